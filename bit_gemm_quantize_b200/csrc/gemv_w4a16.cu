@@ -26,8 +26,9 @@
 // One or two tokens take one MMA column tile (8 columns), a lane holding one pair
 // of a token's digits; more take pairs of tiles, digits 0 and 1 of four tokens in
 // one, 2 and 3 in the other, so that a lane holds all digits of its token.
-// A block with an infinity keeps the infinities alone (as +-1, F infinite), one
-// with a NaN has F = NaN.
+// A block with a NaN has F = NaN.  A token with a block of infinities is multiplied
+// again in fp32 (plain_runs), so that infinities, the zeros that they meet among the
+// codes, and each other give what the formula gives.
 //
 // Layout.  A cluster of 1 to 8 CTAs of 16 warps (one CTA per SM) owns a range of
 // columns, a multiple of 8 wide, so that the clusters' shares differ by 8
@@ -68,6 +69,7 @@
 
 #include <cstdint>
 #include <mutex>
+#include <type_traits>
 
 #include "kernels.h"
 #include "moe.h"
@@ -151,8 +153,8 @@ __device__ __forceinline__ void load_tokens(const void* x, int type, int64_t at,
 // 4 h + 3.  Returns the factors of the low and the high pair of digits, which
 // include 1/16 for the 16 q of the weights and 2^-8, so that a value next to the
 // largest fp32 one does not overflow where its high pair rounds up (the output
-// step multiplies by 2^8).
-__device__ __forceinline__ float2 block_digits(const float (&v)[8], uint32_t (&dig)[4][2]) {
+// step multiplies by 2^8).  Sets `plain` where the block is not for digits.
+__device__ __forceinline__ float2 block_digits(const float (&v)[8], uint32_t (&dig)[4][2], bool& plain) {
     uint32_t top = 0u;
 #pragma unroll
     for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(v[j]) & 0x7FFFFFFFu);
@@ -172,9 +174,9 @@ __device__ __forceinline__ float2 block_digits(const float (&v)[8], uint32_t (&d
         F.y = F.x * 65536.0f;
     } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) y[j] = isinf(v[j]) ? (v[j] > 0.0f ? 1u : 0xFFFFFFFFu) : 0u;
-        F.x = __uint_as_float(top == 0x7F800000u ? top : 0x7FC00000u);
-        F.y = 0.0f;
+        for (int j = 0; j < 8; ++j) y[j] = 0u;
+        F.x = F.y = __uint_as_float(0x7FC00000u);
+        plain = top == 0x7F800000u;
     }
     // signed digits: with 0x80 added to the three lower bytes (carries included)
     // and taken off again, each byte is its digit
@@ -198,6 +200,8 @@ __device__ __forceinline__ float2 block_digits(const float (&v)[8], uint32_t (&d
 struct Rows {
     int32_t src[kMaxRows];
     int32_t dst[kMaxRows];
+    // whether this CTA, and any of the cluster, has met a block that is not for digits
+    int plain, plain_all;
 };
 
 // A run: one expert's weights, up to rows_of(NT) tokens, a range of columns.
@@ -211,7 +215,7 @@ struct Run {
 // The digits and factors of a run's tokens for the blocks kb0 .. kb1 - 1: two
 // (token, block) pairs per warp step, 16 lanes each; lane (xt, xw) of a pair has
 // the 8 values that word xw of the weights of lanes t = xt meets.
-__device__ __noinline__ void stage_tokens(const void* x, int type, int64_t ldx, const int32_t* src, int m_rows, int kb0,
+__device__ __noinline__ void stage_tokens(const void* x, int type, int64_t ldx, Rows& rows, int m_rows, int kb0,
                                           int kb1, uint4* xs, float2* fs) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int xt = lane & 3, xh = (lane >> 2) & 1, xw = lane >> 3;
@@ -219,11 +223,13 @@ __device__ __noinline__ void stage_tokens(const void* x, int type, int64_t ldx, 
     for (uint32_t q0 = warp * 2; q0 < pairs; q0 += 2 * kWarps) {
         const uint32_t q = q0 + xh;
         const uint32_t kb = q / uint32_t(m_rows), m = q - kb * m_rows;
-        const int32_t row = q < pairs ? src[m] : -1;
+        const int32_t row = q < pairs ? rows.src[m] : -1;
         float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
         if (row >= 0) load_tokens(x, type, int64_t(row) * ldx + int64_t(kb0 + kb) * 128 + xt * 32 + xw * 8, v);
         uint32_t dig[4][2];
-        const float2 F = block_digits(v, dig);
+        bool plain = false;
+        const float2 F = block_digits(v, dig, plain);
+        if (plain) rows.plain = 1;
         if (q < pairs) {
             uint2* dst = reinterpret_cast<uint2*>(xs + ((kb * 2 + (xw >> 1)) * m_rows + m) * 16 + xt) + (xw & 1);
 #pragma unroll
@@ -278,10 +284,74 @@ __device__ __forceinline__ void store_out(const Params& p, int32_t dst, int32_t 
     }
 }
 
+// The tokens (bits, in *found) of a run that have a block that is not for digits.
+__device__ __forceinline__ void find_plain(const void* x, int type, int64_t ldx, const int32_t* src, int m_rows,
+                                           int nkb, uint32_t* found) {
+    const int lane = threadIdx.x & 31, xh = (lane >> 2) & 1, at = (lane & 3) * 32 + (lane >> 3) * 8;
+    for (int q0 = int(threadIdx.x >> 5) * 2; q0 < m_rows * nkb; q0 += 2 * kWarps) {
+        const int q = q0 + xh, m = q / nkb, kb = q - m * nkb;
+        float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+        if (m < m_rows && src[m] >= 0) load_tokens(x, type, src[m] * ldx + kb * 128 + at, v);
+        uint32_t dig[4][2];
+        bool plain = false;
+        block_digits(v, dig, plain);
+        if (plain) atomicOr(found, 1u << m);
+    }
+}
+
+// The outputs of some tokens (bits) of a run, in fp32 altogether: a warp takes four
+// columns, a lane eight codes of each in a chain of products, scaled and added to the
+// lane's sums; the lanes' sums are added last.  The cluster's CTAs share the columns.
+// A token costs about 30 us at K = 4096, N = 22016 (bound by latency); where there is
+// none the kernel is as fast as without this.
+template <bool INT>
+__device__ __forceinline__ void plain_tokens(const Params& p, const Run& run, const Rows& rows, uint32_t tokens) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int C = 1 << p.cluster_log, rank = int(blockIdx.x) & (C - 1);
+    for (; tokens; tokens &= tokens - 1) {
+        const int m = __ffs(int(tokens)) - 1;
+        const int64_t xrow = rows.src[m] * p.ldx;
+        for (int32_t n = run.col0 + (rank * kWarps + warp) * 4; n < run.col1; n += C * kWarps * 4) {
+            float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+            for (int32_t k0 = lane * 8; k0 < p.K; k0 += 256) {
+                float v[8];
+                load_tokens(p.x, p.x_type, xrow + k0, v);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] *= 0x1p-8f;  // as in the factors
+                const int kb = k0 >> 7;
+                const int64_t at = int64_t(p.group_magic ? int(__umulhi(uint32_t(kb), p.group_magic)) : kb) * p.N + n;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const uint32_t word =
+                        *reinterpret_cast<const uint32_t*>(run.w + int64_t(n + c) * (p.K >> 1) + (k0 >> 1)) ^ 0x88888888u;
+                    float sum = 0.0f;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {  // the low nibbles, then the high ones: q + 8, behind 2^23
+                        const uint32_t code = word >> (j < 4 ? 8 * j : 8 * j - 28);
+                        sum = __fmaf_rn(v[j], __uint_as_float((code & 15u) | 0x4B000000u) - 8388616.0f, sum);
+                    }
+                    acc[c] = __fmaf_rn(INT ? float(static_cast<const int16_t*>(run.scales)[at + c])
+                                           : static_cast<const float*>(run.scales)[at + c],
+                                       sum, acc[c]);
+                }
+            }
+            Cols<4> out;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) acc[c] += __shfl_xor_sync(0xffffffffu, acc[c], o);
+                out.v[c] = acc[c];
+            }
+            if (lane == 0) store_out(p, rows.dst[m], n, out);
+        }
+    }
+}
+
 // One run, with the tokens' digits in NT MMA column tiles (1 for one or two
 // tokens, 2 for four, 4 for eight).
 template <int NT, bool INT>
-__device__ __forceinline__ void run_columns(const Params& p, const Run& run, const Rows& rows, uint8_t* smem) {
+__device__ __forceinline__ void run_columns(const Params& p, const Run& run, Rows& rows, uint8_t* smem) {
     constexpr int kPair = NT == 1 ? 1 : 2;  // tiles worked on together
     constexpr int kPasses = NT / kPair;
     // columns a thread adds up at a time: with few tokens there are too few outputs to give it four
@@ -387,7 +457,7 @@ __device__ __forceinline__ void run_columns(const Params& p, const Run& run, con
 
             if (panels > 1 || b0 == run.col0) {
                 __syncthreads();  // the rows are set; the last panel's tokens have been used
-                stage_tokens(p.x, p.x_type, p.ldx, rows.src, m_rows, kb0, kb1, xs, fs);
+                stage_tokens(p.x, p.x_type, p.ldx, rows, m_rows, kb0, kb1, xs, fs);
             }
             __syncthreads();
 
@@ -406,12 +476,12 @@ __device__ __forceinline__ void run_columns(const Params& p, const Run& run, con
                     if (ckb < kb1 - kb0) {
                         const uint8_t* slot = ring + cslot;
                         uint4 wreg[4];
-                        float sreg[4];
+                        std::conditional_t<INT, int, float> sreg[4];
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             wreg[i] = *reinterpret_cast<const uint4*>(slot + i * 512 + lane * 16);
                             if constexpr (INT)
-                                sreg[i] = float(reinterpret_cast<const int16_t*>(slot + 2048)[g + 8 * i]);
+                                sreg[i] = reinterpret_cast<const int16_t*>(slot + 2048)[g + 8 * i];
                             else
                                 sreg[i] = reinterpret_cast<const float*>(slot + 2048)[g + 8 * i];
                         }
@@ -459,7 +529,7 @@ __device__ __forceinline__ void run_columns(const Params& p, const Run& run, con
                                         v = __fmaf_rn(
                                             __int2float_rn(c[r][kPair - 1][2 * j + 1] * 256 + c[r][kPair - 1][2 * j]),
                                             65536.0f, v);
-                                    acc[r][pass][j] = __fmaf_rn(sreg[2 * r + j], __fmul_rn(F, v), acc[r][pass][j]);
+                                    acc[r][pass][j] = __fmaf_rn(float(sreg[2 * r + j]), __fmul_rn(F, v), acc[r][pass][j]);
                                 }
                         }
                     }
@@ -511,7 +581,10 @@ __device__ __forceinline__ void run_columns(const Params& p, const Run& run, con
         if (direct) continue;
         // the batch's sums: of all CTAs of the cluster in turn
         const int quads = (b1 - b0) / 4, n_out = quads * m_rows;
-        if (C > 1) cg::this_cluster().sync();  // every CTA's sums are there
+        if (C > 1) {
+            cg::this_cluster().sync();  // every CTA's sums are there
+            if (rows.plain && int(threadIdx.x) < C) *cg::this_cluster().map_shared_rank(&rows.plain_all, threadIdx.x) = 1;
+        }
         for (int o = rank * kThreads + int(threadIdx.x); o < n_out; o += C * kThreads) {
             const int m = int(uint32_t(o) / uint32_t(quads)), n = (o - m * quads) * 4, at = m * batch + n;
             Cols<4> sum{};
@@ -525,20 +598,102 @@ __device__ __forceinline__ void run_columns(const Params& p, const Run& run, con
     }
 }
 
+// What a CTA's threads share about the call: each expert's first routed row, the
+// row chunks before its own, its weights and scales; the first routed rows, looked
+// up early; the rows of the run at hand.
+template <bool GROUPED>
+struct Tables {
+    static constexpr int kE = GROUPED ? kMaxExperts : 0, kEarly = GROUPED ? kEarlyRows : 1;
+    int32_t off[kE + 1], chunk[kE + 1];
+    const uint8_t* w[kE + 1];
+    const void* scales[kE + 1];
+    int32_t early_src[kEarly], early_dst[kEarly];
+    int bad;
+    Rows rows;
+    // the cluster's first item, its next one and the one behind its last
+    uint32_t chunks, first, it, it_end, found;
+};
+
+// The next run of the items it .. it_end - 1 (`it` moves behind it), and its rows.
+template <int NT, bool GROUPED>
+__device__ __forceinline__ Run next_run(const Params& p, Tables<GROUPED>& tab, uint32_t chunks, uint32_t& it,
+                                        uint32_t it_end) {
+    constexpr uint32_t kRows = rows_of(NT);
+    const uint32_t units = uint32_t(p.N) >> 3;  // columns in eights
+    Run run;
+    const uint32_t chunk = !GROUPED && chunks == 1 ? 0u : it / units;
+    const uint32_t unit0 = it - chunk * units;
+    const uint32_t unit1 = min(units, unit0 + (it_end - it));
+    it += unit1 - unit0;
+    int32_t r0;
+    if constexpr (GROUPED) {
+        int e = 0, e_hi = p.E - 1;  // the last expert whose first chunk is <= chunk
+        while (e < e_hi) {
+            const int mid = (e + e_hi + 1) >> 1;
+            if (tab.chunk[mid] <= int32_t(chunk)) e = mid; else e_hi = mid - 1;
+        }
+        r0 = tab.off[e] + int32_t((chunk - uint32_t(tab.chunk[e])) * kRows);
+        run.m_rows = min(int32_t(kRows), tab.off[e + 1] - r0);
+        run.w = tab.w[e];
+        run.scales = tab.scales[e];
+    } else {
+        r0 = int32_t(chunk * kRows);
+        run.m_rows = min(int32_t(kRows), int32_t(p.R) - r0);
+        run.w = p.w;
+        run.scales = p.scales;
+    }
+    run.col0 = int32_t(unit0 * 8);
+    run.col1 = int32_t(unit1 * 8);
+
+    __syncthreads();  // the last run's rows have been used
+    if (int(threadIdx.x) < run.m_rows) {
+        const int32_t r = r0 + int32_t(threadIdx.x);
+        int32_t src = r, dst = r;
+        if constexpr (GROUPED) {
+            if (r < kEarlyRows) {
+                src = tab.early_src[r];
+                dst = tab.early_dst[r];
+            } else {
+                if (p.row_index) src = p.row_index[r];
+                if (p.out_row) dst = p.out_row[r];
+            }
+        }
+        if (src < 0 || src >= p.x_rows) {
+            src = -1;
+            atomicExch(p.status, kStatusInvalidArg);
+        }
+        if (dst < 0 || dst >= p.y_rows) {
+            dst = -1;
+            atomicExch(p.status, kStatusInvalidArg);
+        }
+        tab.rows.src[threadIdx.x] = src;
+        tab.rows.dst[threadIdx.x] = dst;
+    }
+    return run;
+}
+
+// The CTA's runs once more, for the tokens that are not for digits: their outputs are
+// written again, over what the digits gave.
+template <int NT, bool INT, bool GROUPED>
+__device__ __noinline__ void plain_runs(const Params& p, Tables<GROUPED>& tab) {
+    uint32_t it = tab.first;
+    while (it < tab.it_end) {
+        const Run run = next_run<NT, GROUPED>(p, tab, tab.chunks, it, tab.it_end);
+        if (threadIdx.x == 0) tab.found = 0u;
+        __syncthreads();
+        find_plain(p.x, p.x_type, p.ldx, tab.rows.src, run.m_rows, p.K >> 7, &tab.found);
+        __syncthreads();
+        plain_tokens<INT>(p, run, tab.rows, tab.found);
+    }
+}
+
 // One kernel for each number of token tiles: together, three bodies share one
 // register allocation and spill (8 tokens 25 -> 28 us).
 template <int NT, bool INT, bool GROUPED>
-__global__ void __launch_bounds__(kThreads, 1) w4a16_kernel(const Params p) {
+__global__ void __launch_bounds__(kThreads, 1) w4a16_kernel(const __grid_constant__ Params p) {
     constexpr uint32_t kRows = rows_of(NT);
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ Rows rows;
-    constexpr int kE = GROUPED ? kMaxExperts : 0, kEarly = GROUPED ? kEarlyRows : 1;
-    __shared__ int32_t off_s[kE + 1];    // first routed row of each expert
-    __shared__ int32_t chunk_s[kE + 1];  // row chunks before each expert's
-    __shared__ const uint8_t* w_s[kE + 1];
-    __shared__ const void* scale_s[kE + 1];
-    __shared__ int32_t early_src[kEarly], early_dst[kEarly];
-    __shared__ int bad_s;
+    __shared__ Tables<GROUPED> tab;
     const int lane = threadIdx.x & 31;
     const uint32_t units = uint32_t(p.N) >> 3;  // columns in eights
 
@@ -551,8 +706,8 @@ __global__ void __launch_bounds__(kThreads, 1) w4a16_kernel(const Params p) {
         if (threadIdx.x >= kThreads - kEarlyRows) {
             const int r = int(threadIdx.x) - (kThreads - kEarlyRows);
             if (r < p.R) {
-                early_src[r] = p.row_index ? p.row_index[r] : r;
-                early_dst[r] = p.out_row ? p.out_row[r] : r;
+                tab.early_src[r] = p.row_index ? p.row_index[r] : r;
+                tab.early_dst[r] = p.out_row ? p.out_row[r] : r;
             }
         }
         if (threadIdx.x < 32) {
@@ -570,8 +725,8 @@ __global__ void __launch_bounds__(kThreads, 1) w4a16_kernel(const Params p) {
                     if (b > a && (!w || !sc || (reinterpret_cast<uintptr_t>(w) & 15u) != 0 ||
                                   (reinterpret_cast<uintptr_t>(sc) & 3u) != 0))
                         bad = 1;
-                    w_s[e] = w;
-                    scale_s[e] = sc;
+                    tab.w[e] = w;
+                    tab.scales[e] = sc;
                 }
                 bad = __any_sync(0xffffffffu, bad);
                 if (bad) break;
@@ -582,21 +737,21 @@ __global__ void __launch_bounds__(kThreads, 1) w4a16_kernel(const Params p) {
                     if (lane >= o) incl += v;
                 }
                 if (e < p.E) {
-                    off_s[e] = int32_t(a);
-                    off_s[e + 1] = int32_t(b);
-                    chunk_s[e + 1] = before + incl;
+                    tab.off[e] = int32_t(a);
+                    tab.off[e + 1] = int32_t(b);
+                    tab.chunk[e + 1] = before + incl;
                 }
                 before += __shfl_sync(0xffffffffu, incl, 31);
             }
             if (lane == 0) {
-                chunk_s[0] = 0;
-                bad_s = bad;
+                tab.chunk[0] = 0;
+                tab.bad = bad;
                 if (bad && blockIdx.x == 0) atomicExch(p.status, kStatusInvalidArg);
             }
         }
         __syncthreads();
-        if (bad_s) return;
-        chunks = uint32_t(chunk_s[p.E]);
+        if (tab.bad) return;
+        chunks = uint32_t(tab.chunk[p.E]);
     }
 
     // ---- this cluster's range of (expert, row chunk, eight columns) items, columns
@@ -624,58 +779,28 @@ __global__ void __launch_bounds__(kThreads, 1) w4a16_kernel(const Params p) {
         it = share(chunks * units, clusters, id);
         it_end = share(chunks * units, clusters, id + 1);
     }
-    while (it < it_end) {
-        const uint32_t chunk = !GROUPED && chunks == 1 ? 0u : it / units;
-        const uint32_t unit0 = it - chunk * units;
-        const uint32_t unit1 = min(units, unit0 + (it_end - it));
-        it += unit1 - unit0;
-        Run run;
-        int32_t r0;
-        if constexpr (GROUPED) {
-            int e = 0, e_hi = p.E - 1;  // the last expert whose first chunk is <= chunk
-            while (e < e_hi) {
-                const int mid = (e + e_hi + 1) >> 1;
-                if (chunk_s[mid] <= int32_t(chunk)) e = mid; else e_hi = mid - 1;
-            }
-            r0 = off_s[e] + int32_t((chunk - uint32_t(chunk_s[e])) * kRows);
-            run.m_rows = min(int32_t(kRows), off_s[e + 1] - r0);
-            run.w = w_s[e];
-            run.scales = scale_s[e];
-        } else {
-            r0 = int32_t(chunk * kRows);
-            run.m_rows = min(int32_t(kRows), int32_t(p.R) - r0);
-            run.w = p.w;
-            run.scales = p.scales;
-        }
-        run.col0 = int32_t(unit0 * 8);
-        run.col1 = int32_t(unit1 * 8);
-
-        __syncthreads();  // the last run's rows have been used
-        if (int(threadIdx.x) < run.m_rows) {
-            const int32_t r = r0 + int32_t(threadIdx.x);
-            int32_t src = r, dst = r;
-            if constexpr (GROUPED) {
-                if (r < kEarlyRows) {
-                    src = early_src[r];
-                    dst = early_dst[r];
-                } else {
-                    if (p.row_index) src = p.row_index[r];
-                    if (p.out_row) dst = p.out_row[r];
-                }
-            }
-            if (src < 0 || src >= p.x_rows) {
-                src = -1;
-                atomicExch(p.status, kStatusInvalidArg);
-            }
-            if (dst < 0 || dst >= p.y_rows) {
-                dst = -1;
-                atomicExch(p.status, kStatusInvalidArg);
-            }
-            rows.src[threadIdx.x] = src;
-            rows.dst[threadIdx.x] = dst;
-        }
-        run_columns<NT, INT>(p, run, rows, smem);
+    if (it >= it_end) return;
+    if (threadIdx.x == 0) {
+        tab.rows.plain = tab.rows.plain_all = 0;
+        tab.chunks = chunks;
+        tab.first = tab.it = it;
+        tab.it_end = it_end;
     }
+    if constexpr (GROUPED) {  // the place among the items in shared memory: kept in registers it spills the sums
+        __syncthreads();
+        while (tab.it < tab.it_end) {
+            it = tab.it;
+            const Run run = next_run<NT, GROUPED>(p, tab, tab.chunks, it, tab.it_end);
+            if (threadIdx.x == 0) tab.it = it;  // (every thread has read it)
+            run_columns<NT, INT>(p, run, tab.rows, smem);
+        }
+    } else {
+        while (it < it_end) {
+            const Run run = next_run<NT, GROUPED>(p, tab, chunks, it, it_end);
+            run_columns<NT, INT>(p, run, tab.rows, smem);
+        }
+    }
+    if (p.cluster_log ? tab.rows.plain_all : tab.rows.plain) plain_runs<NT, INT, GROUPED>(p, tab);
 }
 
 // The clusters of 2^log CTAs that the device holds at once.

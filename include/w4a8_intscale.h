@@ -530,8 +530,8 @@ W4A8_API w4a8_status moe_combine_backward(const void* d_out, int32_t d_dtype, in
  * Each block of 128 values of a token enters as integers of 30 bits and a sign
  * relative to the block's largest magnitude (an error of at most 2^-30 of it a
  * value; none where a bf16 or fp16 value is at least 2^-19 of it).  Sums over a
- * block are exact, scales and sums over the blocks fp32.  A block with a NaN
- * gives NaN; beside an infinity the block's finite values do not count.
+ * block are exact, scales and sums over the blocks fp32.  Infinities and NaN give
+ * what the formula gives (a token that holds infinities is multiplied in fp32).
  * Meant for decode: up to 8 tokens share one pass over the weights, more take
  * further passes.
  * x, x_dtype  device, [M, ldx] of W4A8_F32, W4A8_F16 or W4A8_BF16, 16-byte aligned

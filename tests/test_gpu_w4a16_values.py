@@ -1,0 +1,135 @@
+"""Values that the products of unquantized tokens with 4-bit weights have to
+keep: infinities and NaN, single codes, single values over the exponent range,
+blocks of a few large values among small ones.  Every form of the kernel is
+reached: it has one for up to 2, 4 and 8 tokens of a pass, each dense and per
+expert, with float and with integer scales, and takes K whole, split over a
+cluster or in panels.
+
+Tolerance (units of 2^-24, u).  A token's block of 128 values is held as
+integers, off by at most 2^-30 of the block's largest magnitude a value; sums
+over a block are exact.  Each pair of digits is converted to fp32 (1 u of the
+high pair's sum, which the products' magnitudes bound; the low pair is at most
+2^-14 of the largest value a product) and joined (1 u); scales and factors enter
+by one FMA a block (1 u of a partial sum), and the sums of up to 16 warps, 8
+CTAs and the panels of K are added (1 u each).  The blocks that are multiplied in
+fp32 instead take chains of 32 FMAs, 4 adds and one FMA a block.
+"""
+import numpy as np
+import pytest
+import torch
+
+import bit_gemm_quantize_b200 as bgq
+
+pytestmark = pytest.mark.gpu
+
+DT = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
+U = 2.0 ** -24
+TOKENS = (1, 2, 3, 4, 8, 11)
+
+
+def _pack(q):
+    """Packed bytes [N, K/2] of int codes [N, K]: code j of each word of eight in byte j mod 4, low nibble first."""
+    b = (q & 15).astype(np.uint8).reshape(q.shape[0], -1, 2, 4)
+    return torch.from_numpy((b[:, :, 0] | b[:, :, 1] << 4).reshape(q.shape[0], -1))
+
+
+def _call(form, x, q, scale, kind, alpha=1024, out="f32"):
+    """y of tokens x (a CUDA tensor) with codes q [N, K] and scales [K/128, N] (float, or integers over alpha), dense or
+    as the only expert with rows."""
+    dev = x.device
+    packed = _pack(q).to(dev)
+    s = torch.from_numpy(scale.astype(np.float32 if kind == "float" else np.int16)).to(dev)
+    kw = dict(s_g=s) if kind == "float" else dict(S=s, alpha=alpha)
+    if form == "dense":
+        return bgq.w4a16_gemv(x, packed, out=out, **kw)
+    off = torch.tensor([0, x.shape[0]], dtype=torch.int64, device=dev)
+    kw = {k: [v] if isinstance(v, torch.Tensor) else v for k, v in kw.items()}
+    return bgq.w4a16_gemv_grouped(x, None, off, [packed], out=out, **kw)
+
+
+def _scales(rng, K, N, kind):
+    return rng.uniform(0.001, 0.02, (K // 128, N)).astype(np.float32) if kind == "float" else rng.integers(
+        1, 30, (K // 128, N))
+
+
+def _definition(x, q, scale, kind, alpha=1024):
+    """sum_k x q s in 64 bits, product by product (so that infinities and NaN meet as the formula has them), and
+    sum |x q s| of the finite ones."""
+    s = scale.astype(np.float64) / (1 if kind == "float" else alpha)
+    w = q * np.repeat(s.T, 128, axis=1)
+    xh = x.double().cpu().numpy()
+    with np.errstate(invalid="ignore"):
+        y = np.stack([(row[None] * w).sum(1) for row in xh])
+    mag = np.abs(np.where(np.isfinite(xh), xh, 0.0)) @ np.abs(w).T
+    return y, mag
+
+
+def _same(got, ref, mag, slack_of_mag, absolute=0.0):
+    """Infinities and NaN where the definition has them, the finite ones within slack."""
+    got = got.double().cpu().numpy()
+    assert np.array_equal(np.isnan(got), np.isnan(ref))
+    inf = np.isinf(ref)
+    assert np.array_equal(got[inf], ref[inf]) and not np.isinf(got[~inf]).any()
+    fin = np.isfinite(ref)
+    slack = np.broadcast_to(slack_of_mag * mag + absolute, ref.shape)
+    err = np.abs(got[fin] - ref[fin])
+    assert np.all(err <= slack[fin]), float((err / slack[fin]).max())
+
+
+def _block_slack(x, q, scale, kind, alpha=1024):
+    """The integers' part of the tolerance: 2^-30 of each block's largest value for every product, and the low pair's
+    conversions (at most 2^-14 of the largest value a product, 1 u a block in a chain of them)."""
+    s = scale.astype(np.float64) / (1 if kind == "float" else alpha)
+    w = np.abs(q * np.repeat(s.T, 128, axis=1)).reshape(q.shape[0], -1, 128).sum(2)
+    xh = np.abs(x.double().cpu().numpy())
+    top = np.where(np.isfinite(xh), xh, 0.0).reshape(xh.shape[0], -1, 128).max(2)
+    n = w.shape[1]
+    return (2.0 ** -30 + (n + 2) * U * 2.0 ** -14) * (top @ w.T)
+
+
+def _chain(K):
+    return (K // 128 + 2 + 16 + 8 + 8 + 1 + 37) * U  # 37: a block multiplied in fp32
+
+
+@pytest.mark.parametrize("form", ["dense", "experts"])
+@pytest.mark.parametrize("kind", ["float", "int"])
+@pytest.mark.parametrize("dt", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("codes,values,want", [
+    ((2, -1), (1, 1), "nan"), ((3, -1), (1, -1), "+"), ((3, 0), (1, 1), "nan"), ((3, 2), (1, 1), "+"),
+    ((-3, -2), (1, 1), "-"), ((1, 1), (1, -1), "nan"), ((0, 0), (1, 1), "nan"), ((-8, 7), (-1, 1), "+")])
+def test_two_infinities_of_a_block(cuda_device, form, kind, dt, codes, values, want):
+    K, N = 256, 16
+    for M in TOKENS:
+        x = torch.zeros(M, K)
+        x[:, ::3] = 0.25
+        x[M - 1, 130], x[M - 1, 201] = values[0] * float("inf"), values[1] * float("inf")
+        q = np.ones((N, K), np.int64)
+        q[:, 130], q[:, 201] = codes
+        y = _call(form, x.to(DT[dt]).to(cuda_device), q, np.ones((2, N)), kind)
+        last = y[M - 1].cpu()
+        assert torch.isnan(last).all() if want == "nan" else torch.isinf(last).all() and (last > 0).all() == (want == "+")
+        assert torch.isfinite(y[:M - 1]).all()
+
+
+@pytest.mark.parametrize("form", ["dense", "experts"])
+@pytest.mark.parametrize("kind", ["float", "int"])
+@pytest.mark.parametrize("dt", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("M,K,N", [(1, 256, 24), (2, 4096, 1048), (3, 512, 40), (4, 11008, 72), (8, 1024, 136),
+                                   (8, 16384, 40), (11, 384, 520)])
+def test_infinities_and_nan(cuda_device, form, kind, dt, M, K, N):
+    """Tokens with none, one or several infinities in a block, with NaN beside them, and blocks full of them."""
+    rng = np.random.default_rng(M + K)
+    x = rng.standard_normal((M, K)).astype(np.float32)
+    for m in range(0, M, 2):
+        at = 128 * rng.integers(K // 128) + rng.permutation(128)[:rng.integers(1, 5)]
+        x[m, at] = rng.choice([-np.inf, np.inf], at.size)
+    if M > 2:
+        x[2, :128] = np.inf
+        x[M - 2, rng.integers(K, size=2)] = np.nan, np.inf
+    q = rng.integers(-8, 8, (N, K))
+    scale = _scales(rng, K, N, kind)
+    x = torch.from_numpy(x).to(DT[dt]).to(cuda_device)
+    y = _call(form, x, q, scale, kind)
+    ref, mag = _definition(x, q, scale, kind)
+    _same(y, ref, mag, _chain(K), _block_slack(x, q, scale, kind))
+    assert bgq.device_status() == 0
