@@ -18,7 +18,11 @@
 // largest magnitude.  fp16 and bf16 values that are at least 2^-19 or 2^-22 of
 // the block's largest, and fp32 values at least 2^-6 of it, are kept exactly; an
 // fp32 sum of the products would round at 2^-24 of the largest one.  (Blocks whose
-// largest value is below 2^-108 keep fewer bits.)  v is cut into
+// largest value is below 2^-108 keep fewer bits.)  The cut is relative to the largest
+// value, also where a code of 0 keeps that one out of the product: a token with a
+// block of a few large values over much smaller ones is multiplied again in fp32
+// (few_large, plain_runs), so that elsewhere a cut is within 2^-20 of the largest of
+// the eight values around it, or of the average of the block.  v is split into
 // four signed 8-bit digits, each a column of the MMA, so all sums over a block
 // are exact in int32.  Pairs of digits are joined exactly (c1 * 256 + c0 < 2^30),
 // converted to fp32 and scaled:
@@ -27,8 +31,8 @@
 // of a token's digits; more take pairs of tiles, digits 0 and 1 of four tokens in
 // one, 2 and 3 in the other, so that a lane holds all digits of its token.
 // A block with a NaN has F = NaN.  A token with a block of infinities is multiplied
-// again in fp32 (plain_runs), so that infinities, the zeros that they meet among the
-// codes, and each other give what the formula gives.
+// again in fp32, too, so that infinities, the zeros that they meet among the codes, and
+// each other give what the formula gives.
 //
 // Layout.  A cluster of 1 to 8 CTAs of 16 warps (one CTA per SM) owns a range of
 // columns, a multiple of 8 wide, so that the clusters' shares differ by 8
@@ -148,20 +152,50 @@ __device__ __forceinline__ void load_tokens(const void* x, int type, int64_t at,
     }
 }
 
+// Whether a block of a token (laid out as for block_digits, E the exponent field of
+// its largest magnitude, 2^(E - 127) = P) has values that digits would cut and is held
+// up by so few large ones that the cut may count: with every magnitude taken at most
+// as c = 2^-8 P, its nonzero values average less than c / 4.
+__device__ __forceinline__ bool few_large(float v0, float v1, float v2, float v3, float v4, float v5, float v6, float v7,
+                                       int type, int E) {
+    const float v[8] = {v0, v1, v2, v3, v4, v5, v6, v7};
+    // magnitudes from 2^-6 P (fp32), 2^-19 P (fp16) and 2^-22 P (bf16) on keep all their bits
+    const uint32_t keep = uint32_t(max(E - (type == kElemF32 ? 6 : type == kElemF16 ? 19 : 22), 1)) << 23;
+    const float inv_c = __uint_as_float(uint32_t(262 - E) << 23);
+    bool cut = false;
+    float sum = 0.0f;  // of magnitudes, in c / 4, less the number of values that are not 0
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const float a = fabsf(v[j]);
+        cut |= a != 0.0f && __float_as_uint(a) < keep;
+        sum += 4.0f * __saturatef(a * inv_c) - (a != 0.0f ? 1.0f : 0.0f);
+    }
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1)
+        if (o != 4) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    const unsigned lanes = (threadIdx.x & 4) ? 0xF0F0F0F0u : 0x0F0F0F0Fu;  // the block's
+    return (__ballot_sync(0xffffffffu, cut) & lanes) != 0u && sum < 0.0f;
+}
+
 // A block of 128 values of one token, 8 per lane of 16 lanes (those of the warp
 // that agree in bit 2), as digits: dig[d][h] holds digit d of values 4 h ..
 // 4 h + 3.  Returns the factors of the low and the high pair of digits, which
 // include 1/16 for the 16 q of the weights and 2^-8, so that a value next to the
 // largest fp32 one does not overflow where its high pair rounds up (the output
 // step multiplies by 2^8).  Sets `plain` where the block is not for digits.
-__device__ __forceinline__ float2 block_digits(const float (&v)[8], uint32_t (&dig)[4][2], bool& plain) {
+__device__ __forceinline__ float2 block_digits(const float (&v)[8], int type, uint32_t (&dig)[4][2],
+                                               bool& plain) {
     uint32_t top = 0u;
 #pragma unroll
     for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+    const uint32_t own = top;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1)
         if (o != 4) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
     const int E = max(int(top >> 23), 19);  // below, the factor would leave the fp32 range
+    // no need to look closer while every lane's eight values have a large one
+    if (!__all_sync(0xffffffffu, own >= uint32_t(E - 10) << 23))
+        plain = few_large(v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7], type, E);
     uint32_t y[8];
     float2 F;
     if (E < 255) {
@@ -176,7 +210,7 @@ __device__ __forceinline__ float2 block_digits(const float (&v)[8], uint32_t (&d
 #pragma unroll
         for (int j = 0; j < 8; ++j) y[j] = 0u;
         F.x = F.y = __uint_as_float(0x7FC00000u);
-        plain = top == 0x7F800000u;
+        if (top == 0x7F800000u) plain = true;
     }
     // signed digits: with 0x80 added to the three lower bytes (carries included)
     // and taken off again, each byte is its digit
@@ -228,7 +262,7 @@ __device__ __noinline__ void stage_tokens(const void* x, int type, int64_t ldx, 
         if (row >= 0) load_tokens(x, type, int64_t(row) * ldx + int64_t(kb0 + kb) * 128 + xt * 32 + xw * 8, v);
         uint32_t dig[4][2];
         bool plain = false;
-        const float2 F = block_digits(v, dig, plain);
+        const float2 F = block_digits(v, type, dig, plain);
         if (plain) rows.plain = 1;
         if (q < pairs) {
             uint2* dst = reinterpret_cast<uint2*>(xs + ((kb * 2 + (xw >> 1)) * m_rows + m) * 16 + xt) + (xw & 1);
@@ -294,7 +328,7 @@ __device__ __forceinline__ void find_plain(const void* x, int type, int64_t ldx,
         if (m < m_rows && src[m] >= 0) load_tokens(x, type, src[m] * ldx + kb * 128 + at, v);
         uint32_t dig[4][2];
         bool plain = false;
-        block_digits(v, dig, plain);
+        block_digits(v, type, dig, plain);
         if (plain) atomicOr(found, 1u << m);
     }
 }

@@ -529,9 +529,12 @@ W4A8_API w4a8_status moe_combine_backward(const void* d_out, int32_t d_dtype, in
  *   y[m,n] = fl_out(sum_g s[g,n] * sum_{k in g} x[m,k] q_w[k,n]),   s = s_g or S / alpha
  * Each block of 128 values of a token enters as integers of 30 bits and a sign
  * relative to the block's largest magnitude (an error of at most 2^-30 of it a
- * value; none where a bf16 or fp16 value is at least 2^-19 of it).  Sums over a
- * block are exact, scales and sums over the blocks fp32.  Infinities and NaN give
- * what the formula gives (a token that holds infinities is multiplied in fp32).
+ * value, also where the largest value's own code is 0; none where a bf16 or fp16
+ * value is at least 2^-19 of it).  Sums over a block are exact, scales and sums over
+ * the blocks fp32.  A token with a block whose values are nearly all so much smaller
+ * than its largest that this error would be more than 2^-20 of them, or with
+ * infinities, is multiplied in fp32 altogether, which takes longer.  Infinities and
+ * NaN give what the formula gives.
  * Meant for decode: up to 8 tokens share one pass over the weights, more take
  * further passes.
  * x, x_dtype  device, [M, ldx] of W4A8_F32, W4A8_F16 or W4A8_BF16, 16-byte aligned

@@ -133,3 +133,33 @@ def test_infinities_and_nan(cuda_device, form, kind, dt, M, K, N):
     ref, mag = _definition(x, q, scale, kind)
     _same(y, ref, mag, _chain(K), _block_slack(x, q, scale, kind))
     assert bgq.device_status() == 0
+
+
+@pytest.mark.parametrize("form", ["dense", "experts"])
+@pytest.mark.parametrize("kind", ["float", "int"])
+@pytest.mark.parametrize("dt", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("ratio", [30.0, 1e3, 1e4, 3e6])
+@pytest.mark.parametrize("outliers", [1, 5, 20])
+def test_large_values_over_zero_codes(cuda_device, form, kind, dt, ratio, outliers):
+    """A few values far above the rest of their block, where the codes are 0: they are in no product, and what is left is
+    as exact as the products that there are.  Beside them an exact zero or two, eight values without a large one, and
+    blocks without any."""
+    K, N = 384, 40
+    for M in TOKENS:
+        rng = np.random.default_rng(M + outliers)
+        x = rng.standard_normal((M, K)) * (30000.0 / ratio / 3)
+        q = rng.integers(-8, 8, (N, K))
+        for m in range(M):
+            at = rng.permutation(120)
+            block = 128 * (m % 3)
+            x[m, block + at[:outliers]] = rng.uniform(0.5, 1, outliers) * 30000.0
+            x[m, block + at[60:62]] = 0.0
+            q[:, block + at[:outliers]] = 0
+        scale = _scales(rng, K, N, kind)
+        x = torch.from_numpy(x.astype(np.float32)).to(DT[dt]).to(cuda_device)
+        y = _call(form, x, q, scale, kind)
+        ref = x.double().cpu().numpy() @ (q * np.repeat(scale.astype(np.float64).T / (1 if kind == "float" else 1024), 128,
+                                                        axis=1)).T
+        mag = _definition(x, q, scale, kind)[1]
+        _same(y, ref, mag, _chain(K))
+    assert bgq.device_status() == 0
