@@ -90,8 +90,10 @@ def load(path: str = LIB_PATH):
                                             P, I64, P], I32_),
             "moe_route_sort": ([P, I32_, I64, I32_, I32_, P, P, P, P, P], I32_),
             "moe_dispatch": ([P, I32_, I64, I64, I64, P, I32_, I64, P, P], I32_),
+            "moe_dispatch_zeroed": ([P, I32_, I64, I64, I64, P, I32_, I64, P, P], I32_),
             "moe_combine": ([P, I32_, I64, I64, I64, P, P, I64, I32_, P, I32_, P], I32_),
             "moe_combine_backward": ([P, I32_, I64, P, I32_, I64, I64, I64, P, P, I64, I32_, P, P, P], I32_),
+            "moe_combine_backward_zeroed": ([P, I32_, I64, P, I32_, I64, I64, I64, P, P, I64, I32_, P, P, P], I32_),
             "w4a16_gemv": ([P, I32_, I64, I64, I64, P, P, P, I32_, I64, I32_, P, I32_, P], I32_),
             "w4a16_gemv_grouped": ([P, I32_, I64, I64, I64, P, P, P, P, P, P, I32_, I32_, I64, I64, I32_, P, I32_, I64,
                                     P], I32_),
@@ -701,17 +703,19 @@ def moe_route_sort(expert_ids: torch.Tensor, E: int, *, expert_offsets: torch.Te
 def moe_dispatch(x: torch.Tensor, slot_row: torch.Tensor, *, x_r: torch.Tensor | None = None):
     """Token rows x [T, H] (fp32, fp16 or bf16) in expert order: x_r[slot_row[t, s]]
     = x[t]; the rows of dropped slots are zeroed.  x_r [T*top_k, H] unless given
-    (more rows may be; those that no slot names stay as they were).  Its gradient
-    is moe_dispatch_backward."""
+    (more rows may be).  Rows that no slot names (a slot of -1 names none) are zero in
+    a result allocated here and stay as they were in a given one.  Its gradient is
+    moe_dispatch_backward."""
     dt, ld = _float_rows("x", x)
     _need_cuda("slot_row", slot_row, torch.int32, 2)
     T, H = x.shape
     k = slot_row.shape[1]
     if slot_row.shape[0] != T:
         raise ValueError("slot_row must be [T, top_k]")
+    name = "moe_dispatch_zeroed" if x_r is None else "moe_dispatch"
     x_r = _result("x_r", x_r, (T * k if x_r is None else x_r.shape[0], H), x.dtype, x)
     dev = _same_device(x, slot_row, x_r)
-    _launch("moe_dispatch", dev, x.data_ptr(), dt, T, H, ld, slot_row.data_ptr(), k, x_r.shape[0], x_r.data_ptr())
+    _launch(name, dev, x.data_ptr(), dt, T, H, ld, slot_row.data_ptr(), k, x_r.shape[0], x_r.data_ptr())
     return x_r
 
 
@@ -765,8 +769,8 @@ def moe_combine_backward(d_out: torch.Tensor, y: torch.Tensor, weights: torch.Te
     """The gradients of moe_combine: (d_y [R, H] of y's type, d_weights [T, top_k]
     fp32) with d_y[slot_row[t, s]] = weights[t, s] * d_out[t] and d_weights[t, s]
     = <d_out[t], y[slot_row[t, s]]>; a dropped slot's row is zeroed, its weight's
-    gradient is 0.  Rows that no slot names keep what d_y held; a d_y allocated
-    here for a y with more or fewer rows than slots starts as zeros."""
+    gradient is 0.  Rows that no slot names (a slot of -1 names none) are zero in a
+    d_y allocated here and keep what a given one held."""
     dd, ldd = _float_rows("d_out", d_out)
     dy_, ldy = _float_rows("y", y)
     _need_cuda("weights", weights, torch.float32, 2)
@@ -778,12 +782,15 @@ def moe_combine_backward(d_out: torch.Tensor, y: torch.Tensor, weights: torch.Te
         _need_cuda("slot_row", slot_row, torch.int32, 2)
         if slot_row.shape != weights.shape:
             raise ValueError("weights and slot_row must both be [T, top_k]")
-    if d_y is None and R != T * k:  # rows beyond the slots'
+    name = "moe_combine_backward"
+    if d_y is None and R > T * k:  # more rows than the call would clear beside its own work
         d_y = torch.zeros((R, H), dtype=y.dtype, device=y.device)
+    elif d_y is None and slot_row is not None:
+        name = "moe_combine_backward_zeroed"
     d_y = _result("d_y", d_y, (R, H), y.dtype, y)
     d_weights = _result("d_weights", d_weights, (T, k), torch.float32, y)
     dev = _same_device(d_out, y, weights, slot_row, d_y, d_weights)
-    _launch("moe_combine_backward", dev, d_out.data_ptr(), dd, ldd, y.data_ptr(), dy_, R, H, ldy, _address(slot_row),
+    _launch(name, dev, d_out.data_ptr(), dd, ldd, y.data_ptr(), dy_, R, H, ldy, _address(slot_row),
             weights.data_ptr(), T, k, d_y.data_ptr(), d_weights.data_ptr())
     return d_y, d_weights
 

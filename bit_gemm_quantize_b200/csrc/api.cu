@@ -784,12 +784,13 @@ w4a8_status moe_route_sort(const void* expert_ids, int32_t ids64, int64_t T, int
     return W4A8_OK;
 }
 
-w4a8_status moe_dispatch(const void* x, int32_t x_dtype, int64_t T, int64_t H, int64_t ldx, const int32_t* slot_row,
-                         int32_t top_k, int64_t R, void* x_r, void* stream) {
+static w4a8_status dispatch(const void* x, int32_t x_dtype, int64_t T, int64_t H, int64_t ldx, const int32_t* slot_row,
+                            int32_t top_k, int64_t R, void* x_r, bool zeroed, void* stream) {
     const int elem = elem_of(x_dtype);
     if (elem < 0) return W4A8_ERR_DTYPE;
     w4a8_status st = check_rows(T, top_k, R, H, ldx, H);
     if (st != W4A8_OK) return st;
+    if (zeroed && R > T * top_k) return W4A8_ERR_SHAPE;
     if (T == 0) return W4A8_OK;
     if (!x || !slot_row || (R > 0 && !x_r)) return W4A8_ERR_INVALID_ARG;
     if (!aligned_to(x, elem_bytes(elem)) || !aligned_to(x_r, elem_bytes(elem)) || !aligned4(slot_row))
@@ -805,9 +806,20 @@ w4a8_status moe_dispatch(const void* x, int32_t x_dtype, int64_t T, int64_t H, i
     p.R = R;
     p.H = H;
     p.top_k = top_k;
+    p.zeroed = zeroed;
     p.status = dev.status;
     W4A8_CUDA_TRY(w4a8::moe::launch_dispatch(p, elem, dev.sms, static_cast<cudaStream_t>(stream)));
     return W4A8_OK;
+}
+
+w4a8_status moe_dispatch(const void* x, int32_t x_dtype, int64_t T, int64_t H, int64_t ldx, const int32_t* slot_row,
+                         int32_t top_k, int64_t R, void* x_r, void* stream) {
+    return dispatch(x, x_dtype, T, H, ldx, slot_row, top_k, R, x_r, false, stream);
+}
+
+w4a8_status moe_dispatch_zeroed(const void* x, int32_t x_dtype, int64_t T, int64_t H, int64_t ldx,
+                                const int32_t* slot_row, int32_t top_k, int64_t R, void* x_r, void* stream) {
+    return dispatch(x, x_dtype, T, H, ldx, slot_row, top_k, R, x_r, true, stream);
 }
 
 w4a8_status moe_combine(const void* y, int32_t y_dtype, int64_t R, int64_t H, int64_t ldy, const int32_t* slot_row,
@@ -838,13 +850,14 @@ w4a8_status moe_combine(const void* y, int32_t y_dtype, int64_t R, int64_t H, in
     return W4A8_OK;
 }
 
-w4a8_status moe_combine_backward(const void* d_out, int32_t d_dtype, int64_t ldd, const void* y, int32_t y_dtype,
-                                 int64_t R, int64_t H, int64_t ldy, const int32_t* slot_row, const float* weights,
-                                 int64_t T, int32_t top_k, void* d_y, float* d_weights, void* stream) {
+static w4a8_status combine_backward(const void* d_out, int32_t d_dtype, int64_t ldd, const void* y, int32_t y_dtype,
+                                    int64_t R, int64_t H, int64_t ldy, const int32_t* slot_row, const float* weights,
+                                    int64_t T, int32_t top_k, void* d_y, float* d_weights, bool zeroed, void* stream) {
     const int ed = elem_of(d_dtype), ey = elem_of(y_dtype);
     if (ed < 0 || ey < 0) return W4A8_ERR_DTYPE;
     w4a8_status st = check_rows(T, top_k, R, H, ldy, ldd);
     if (st != W4A8_OK) return st;
+    if (zeroed && R > T * top_k) return W4A8_ERR_SHAPE;
     if (T == 0) return W4A8_OK;
     if (!slot_row && R < T * top_k) return W4A8_ERR_SHAPE;
     if (!d_out || (R > 0 && (!y || !d_y)) || !weights || !d_weights) return W4A8_ERR_INVALID_ARG;
@@ -866,9 +879,25 @@ w4a8_status moe_combine_backward(const void* d_out, int32_t d_dtype, int64_t ldd
     p.R = R;
     p.H = H;
     p.top_k = top_k;
+    p.zeroed = zeroed;
     p.status = dev.status;
     W4A8_CUDA_TRY(w4a8::moe::launch_combine_backward(p, ed, ey, dev.sms, static_cast<cudaStream_t>(stream)));
     return W4A8_OK;
+}
+
+w4a8_status moe_combine_backward(const void* d_out, int32_t d_dtype, int64_t ldd, const void* y, int32_t y_dtype,
+                                 int64_t R, int64_t H, int64_t ldy, const int32_t* slot_row, const float* weights,
+                                 int64_t T, int32_t top_k, void* d_y, float* d_weights, void* stream) {
+    return combine_backward(d_out, d_dtype, ldd, y, y_dtype, R, H, ldy, slot_row, weights, T, top_k, d_y, d_weights,
+                            false, stream);
+}
+
+w4a8_status moe_combine_backward_zeroed(const void* d_out, int32_t d_dtype, int64_t ldd, const void* y,
+                                        int32_t y_dtype, int64_t R, int64_t H, int64_t ldy, const int32_t* slot_row,
+                                        const float* weights, int64_t T, int32_t top_k, void* d_y, float* d_weights,
+                                        void* stream) {
+    return combine_backward(d_out, d_dtype, ldd, y, y_dtype, R, H, ldy, slot_row, weights, T, top_k, d_y, d_weights,
+                            true, stream);
 }
 
 w4a8_status w4a16_gemv(const void* x, int32_t x_dtype, int64_t M, int64_t K, int64_t ldx, const uint8_t* w_packed,

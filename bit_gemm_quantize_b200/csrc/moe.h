@@ -41,6 +41,7 @@ struct RowParams {
     float* d_weights;         // combine backward: [T, top_k]
     int64_t T, R, H;
     int32_t top_k;
+    bool zeroed;              // dispatch and combine backward: clear the rows that no slot names
     int* status;
 };
 cudaError_t launch_dispatch(const RowParams& p, int elem, int num_sms, cudaStream_t stream);

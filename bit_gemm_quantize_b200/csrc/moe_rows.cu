@@ -128,6 +128,63 @@ __device__ __forceinline__ int32_t slot_target(const RowParams& p, int32_t f) {
     return -1;
 }
 
+// Rows that no slot names (a slot of -1, or a row outside, leaves one) are known only
+// when all slots have been seen.  Where the caller wants them cleared, the grid's
+// first CTAs do it beside the others, each for kClearRows rows: it counts the rows that
+// are named, and unless all are, marks those among its own and clears the rest.  The
+// others write named rows only, so nothing has to wait.  (Clearing the whole output
+// first would cost a third of a dispatch: 2048 tokens, 2 slots, 8 KB rows.)
+constexpr int kClearRows = 1024;
+
+unsigned clear_ctas(const RowParams& p) {
+    // without slot_row every row of R <= T * top_k is named
+    return p.zeroed && p.slot_row ? unsigned((p.R + kClearRows - 1) / kClearRows) : 0u;
+}
+
+// f(the row that a slot names, 2^31 or more for none), for every slot of this thread.
+template <typename F>
+__device__ __forceinline__ void each_row(const int32_t* slot_row, int32_t n, F&& f) {
+    const auto row = [](int32_t v) { return uint32_t(v >= 0 ? v : -2 - v); };
+    int32_t i = 0;
+    if ((reinterpret_cast<uintptr_t>(slot_row) & 15u) == 0) {
+#pragma unroll 4
+        for (int32_t q = threadIdx.x; q < n / 4; q += kThreads) {
+            const int4 v = __ldg(reinterpret_cast<const int4*>(slot_row) + q);
+            f(row(v.x)), f(row(v.y)), f(row(v.z)), f(row(v.w));
+        }
+        i = n / 4 * 4;
+    }
+    for (i += int32_t(threadIdx.x); i < n; i += kThreads) f(row(__ldg(slot_row + i)));
+}
+
+template <typename V>
+__device__ __noinline__ void clear_unnamed(const int32_t* slot_row, int32_t n, uint32_t R, V* out, int32_t row_len) {
+    __shared__ uint32_t named[kClearRows / 32];
+    __shared__ uint32_t count;
+    if (threadIdx.x < kClearRows / 32) named[threadIdx.x] = 0u;
+    if (threadIdx.x == 0) count = 0u;
+    __syncthreads();
+    uint32_t mine = 0u;
+    each_row(slot_row, n, [&](uint32_t r) { mine += r < R; });
+    mine = __reduce_add_sync(0xffffffffu, mine);
+    if ((threadIdx.x & 31) == 0) atomicAdd(&count, mine);
+    __syncthreads();
+    if (count >= R) return;
+    const uint32_t first = blockIdx.x * uint32_t(kClearRows), rows = min(R - first, uint32_t(kClearRows));
+    each_row(slot_row, n, [&](uint32_t r) {
+        if (r - first < rows) atomicOr(&named[(r - first) >> 5], 1u << ((r - first) & 31u));
+    });
+    __syncthreads();
+    for (uint32_t k = 0; k < rows; k += 32) {
+        uint32_t left = ~named[k >> 5];
+        if (rows - k < 32u) left &= (1u << (rows - k)) - 1u;
+        for (; left; left &= left - 1u) {
+            V* row = out + (int64_t(first + k) + __ffs(int(left)) - 1) * row_len;
+            for (int32_t c = threadIdx.x; c < row_len; c += kThreads) row[c] = V{};
+        }
+    }
+}
+
 // Item g of the grid: a CTA's tokens, `tpt` threads each (a power of two, 32 to
 // 256), and, for the kernels whose columns are independent, one of `chunks`
 // column ranges.
@@ -151,13 +208,17 @@ __device__ __forceinline__ Place place(const RowParams& p, uint32_t g, int tpt_l
 // 16-byte aligned), one item per CTA
 template <typename V, int U, int kLog>
 __global__ void __launch_bounds__(kThreads) dispatch_kernel(const RowParams p, int32_t nv, int64_t ldv, int tpt_log_,
-                                                            uint32_t chunks) {
+                                                            uint32_t chunks, uint32_t clears) {
     const int tpt_log = kLog > 0 ? kLog : tpt_log_;
     griddep_wait();  // x and slot_row may be the previous kernel's output, x_r its input
     if (threadIdx.x == 0) griddep_launch_dependents();
+    if (blockIdx.x < clears) {
+        clear_unnamed(p.slot_row, int32_t(p.T * p.top_k), uint32_t(p.R), static_cast<V*>(p.out), nv);
+        return;
+    }
     const int tpt = 1 << tpt_log, lane = threadIdx.x & (tpt - 1);
     V* dst = static_cast<V*>(p.out);
-    const Place q = place(p, blockIdx.x, tpt_log, chunks);
+    const Place q = place(p, blockIdx.x - clears, tpt_log, chunks);
     if (q.token >= p.T) return;
     const V* src = static_cast<const V*>(p.a) + q.token * ldv;
     const int32_t f0 = q.token * p.top_k;
@@ -244,7 +305,8 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(const RowParams p, in
 
 // ---- combine backward: kSlots slots at a time share the pieces of d_out[t]
 template <typename TD, typename TY, int E, int U, int kSlots, int kLog>
-__global__ void __launch_bounds__(kThreads) combine_backward_kernel(const RowParams p, int tpt_log_, uint32_t items) {
+__global__ void __launch_bounds__(kThreads) combine_backward_kernel(const RowParams p, int tpt_log_, uint32_t items,
+                                                                    uint32_t clears) {
     const int tpt_log = kLog > 0 ? kLog : tpt_log_;
     __shared__ float red[kThreads / 32][kSlots];
     griddep_wait();  // the inputs may be the previous kernel's output, d_y and d_weights its input
@@ -252,7 +314,13 @@ __global__ void __launch_bounds__(kThreads) combine_backward_kernel(const RowPar
     const int tpt = 1 << tpt_log, lane = threadIdx.x & (tpt - 1), warp = threadIdx.x >> 5;
     const TY* y = static_cast<const TY*>(p.b);
     TY* d_y = static_cast<TY*>(p.out);
-    for (uint32_t g = blockIdx.x; g < items; g += gridDim.x) {
+    if (blockIdx.x < clears) {
+        // whole words where the rows are known to be aligned
+        using V = std::conditional_t<E == 1, std::conditional_t<sizeof(TY) == 4, uint32_t, uint16_t>, uint4>;
+        clear_unnamed(p.slot_row, int32_t(p.T * p.top_k), uint32_t(p.R), reinterpret_cast<V*>(d_y), int32_t(p.H * sizeof(TY) / sizeof(V)));
+        return;
+    }
+    for (uint32_t g = blockIdx.x - clears; g < items; g += gridDim.x - clears) {
         const int32_t token = place(p, g, tpt_log, 1).token;
         const bool live = token < p.T;
         const TD* d = static_cast<const TD*>(p.a) + (live ? token : 0) * p.lda;
@@ -366,8 +434,9 @@ cudaError_t dispatch_t(const RowParams& p, int64_t nv, int64_t ldv, int num_sms,
     if (e != cudaSuccess) return e;
     // not the CTAs that the device holds at once: one per item was faster (14.3
     // against 16.0 us, 2048 tokens, 8 slots, rows of 4 KB)
-    const LaunchPdl lc(s.items, kThreads, 0, stream);
-    return cudaLaunchKernelEx(&lc.cfg, kern, p, int32_t(nv), ldv, s.tpt_log, s.chunks);
+    const unsigned clears = clear_ctas(p);
+    const LaunchPdl lc(s.items + clears, kThreads, 0, stream);
+    return cudaLaunchKernelEx(&lc.cfg, kern, p, int32_t(nv), ldv, s.tpt_log, s.chunks, clears);
 }
 
 template <typename TY, typename TO, int E, int U, int kSlots, int kLog>
@@ -407,8 +476,12 @@ cudaError_t backward_e(const RowParams& p, int num_sms, cudaStream_t stream) {
     constexpr auto kern = combine_backward_kernel<TD, TY, E, U, kSlots, kLog>;
     const cudaError_t e = shape_of<kern>(p.H / E, U, p.T, false, num_sms, &s, kLog);
     if (e != cudaSuccess) return e;
-    const LaunchPdl lc(s.grid, kThreads, 0, stream);
-    return cudaLaunchKernelEx(&lc.cfg, kern, p, s.tpt_log, s.items);
+    // the clearing CTAs take the place of others that the device would hold at once
+    const unsigned clears = clear_ctas(p);
+    unsigned grid = s.grid;
+    if (grid < s.items) grid = grid > 2 * clears ? grid - clears : grid / 2;
+    const LaunchPdl lc(grid + clears, kThreads, 0, stream);
+    return cudaLaunchKernelEx(&lc.cfg, kern, p, s.tpt_log, s.items, clears);
 }
 
 template <typename TD, typename TY>

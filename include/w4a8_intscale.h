@@ -490,6 +490,14 @@ W4A8_API w4a8_status moe_dispatch(const void* x, int32_t x_dtype, int64_t T, int
                                   const int32_t* slot_row, int32_t top_k, int64_t R, void* x_r, void* stream);
 
 /*
+ * moe_dispatch into new memory: rows of x_r that no slot names (a slot of -1, or
+ * one outside [0, R), leaves one) are zeroed too, in the same launch.
+ * R <= T * top_k (W4A8_ERR_SHAPE).
+ */
+W4A8_API w4a8_status moe_dispatch_zeroed(const void* x, int32_t x_dtype, int64_t T, int64_t H, int64_t ldx,
+                                         const int32_t* slot_row, int32_t top_k, int64_t R, void* x_r, void* stream);
+
+/*
  * The experts' outputs back in token order, weighted:
  *   out[t, :] = fl_out(sum_s weights[t,s] * y[r(t,s), :])    (fp32, slot order)
  * with r(t,s) = slot_row[t,s], or t * top_k + s when slot_row is NULL (outputs
@@ -520,6 +528,15 @@ W4A8_API w4a8_status moe_combine_backward(const void* d_out, int32_t d_dtype, in
                                           int32_t y_dtype, int64_t R, int64_t H, int64_t ldy,
                                           const int32_t* slot_row, const float* weights, int64_t T, int32_t top_k,
                                           void* d_y, float* d_weights, void* stream);
+
+/*
+ * moe_combine_backward into new memory: rows of d_y that no slot names are zeroed
+ * too, in the same launch.  R <= T * top_k (W4A8_ERR_SHAPE).
+ */
+W4A8_API w4a8_status moe_combine_backward_zeroed(const void* d_out, int32_t d_dtype, int64_t ldd, const void* y,
+                                                 int32_t y_dtype, int64_t R, int64_t H, int64_t ldy,
+                                                 const int32_t* slot_row, const float* weights, int64_t T,
+                                                 int32_t top_k, void* d_y, float* d_weights, void* stream);
 
 /*
  * Products of a few unquantized tokens with the packed 4-bit weights (a layer
