@@ -29,6 +29,24 @@ struct SortParams {
 };
 cudaError_t launch_sort(const SortParams& p, cudaStream_t stream);
 
+// How a sort of n slots is spread over one cluster of at most `most` CTAs (8, the
+// portable number, or 16 where the device can place that many): CTAs, slots of a CTA
+// at most, and whether it keeps them in shared memory.
+constexpr int32_t kMaxKeptSlots = 24576;
+struct SortShape {
+    int ctas;
+    int32_t per_cta;
+    bool keep;
+};
+constexpr SortShape sort_shape(int32_t n, int most) {
+    // one CTA per 1024 slots (4096 slots: 5.4 us, 6.5 with 2048 a CTA; 131072: 15 us
+    // with 16 CTAs, 30 with 8)
+    int ctas = 1;
+    while (ctas < most && int64_t(n) > int64_t(ctas) * 1024) ctas *= 2;
+    const int64_t steps = (int64_t(n) + 31) / 32, per_cta = (steps + ctas - 1) / ctas * 32;
+    return {ctas, int32_t(per_cta), per_cta <= kMaxKeptSlots};
+}
+
 // Rows between token order and expert order (moe_rows.cu).  slot_row NULL:
 // slot f's row is row f.
 struct RowParams {

@@ -40,7 +40,6 @@ constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kBinsMax = kMaxExperts + 1;
 constexpr int kBatch = 8;             // ids in flight per lane
 constexpr int kSlotBytes = 6;         // a slot's place in the sorted order and its mark
-constexpr int kMaxKeptSlots = 24576;  // of a CTA
 
 template <typename ID>
 __device__ __forceinline__ int bin_of(ID id, int32_t E, bool& bad) {
@@ -226,49 +225,81 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(const SortParams p, 
     }
 }
 
-template <typename ID, bool KEEP>
-cudaError_t launch_t(const SortParams& p, int C, int32_t per_cta, cudaStream_t stream) {
-    cudaError_t e = configure_once<sort_kernel<ID, KEEP>>(kSortThreads, kMaxKeptSlots * kSlotBytes);
-    if (e != cudaSuccess) return e;
-    if (C > 8) {  // more than the portable eight CTAs
-        static std::atomic<bool> allowed[64];
-        int dev = 0;
-        if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
-        if (dev < 0 || dev >= 64 || !allowed[dev].load()) {
-            e = cudaFuncSetAttribute(sort_kernel<ID, KEEP>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-            if (e != cudaSuccess) return e;
-            if (dev >= 0 && dev < 64) allowed[dev].store(true);
-        }
-    }
+// The launch of a cluster of C CTAs.
+struct LaunchCluster {
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(unsigned(C));
-    cfg.blockDim = dim3(kSortThreads);
-    cfg.dynamicSmemBytes = KEEP ? size_t(per_cta) * kSlotBytes : 0;
-    cfg.stream = stream;
     cudaLaunchAttribute attr[2]{};
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = unsigned(C);
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, sort_kernel<ID, KEEP>, p, per_cta);
+    LaunchCluster(int C, size_t smem, cudaStream_t stream) {
+        cfg.gridDim = dim3(unsigned(C));
+        cfg.blockDim = dim3(kSortThreads);
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = stream;
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = unsigned(C);
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[1].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 2;
+    }
+    LaunchCluster(const LaunchCluster&) = delete;
+    LaunchCluster& operator=(const LaunchCluster&) = delete;
+};
+
+template <typename ID, bool KEEP>
+cudaError_t launch_t(const SortParams& p, const SortShape& shape, cudaStream_t stream) {
+    const cudaError_t e = configure_once<sort_kernel<ID, KEEP>>(kSortThreads, kMaxKeptSlots * kSlotBytes);
+    if (e != cudaSuccess) return e;
+    const LaunchCluster lc(shape.ctas, KEEP ? size_t(shape.per_cta) * kSlotBytes : 0, stream);
+    return cudaLaunchKernelEx(&lc.cfg, sort_kernel<ID, KEEP>, p, shape.per_cta);
+}
+
+// The most CTAs of a cluster on the current device: 16, more than the portable eight,
+// if it can place them at all (a partition with small GPCs may not).
+template <typename ID>
+cudaError_t most_ctas(int* out) {
+    static std::atomic<int> known[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    *out = known[dev].load();
+    if (*out != 0) return cudaSuccess;
+    *out = 16;
+    const auto ask = [&](auto kern, int smem) {
+        if (*out < 16) return;
+        cudaError_t r = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (r == cudaSuccess) r = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        const LaunchCluster lc(16, size_t(smem), nullptr);
+        int n = 0;
+        if (r == cudaSuccess) r = cudaOccupancyMaxActiveClusters(&n, kern, &lc.cfg);
+        if (r != cudaSuccess || n < 1) {
+            *out = 8;
+            cudaGetLastError();  // not a failure of the call
+        }
+    };
+    ask(sort_kernel<ID, true>, kMaxKeptSlots * kSlotBytes);
+    ask(sort_kernel<ID, false>, kMaxKeptSlots * kSlotBytes);
+    known[dev].store(*out);
+    return cudaSuccess;
+}
+
+template <typename ID>
+cudaError_t launch_id(const SortParams& p, cudaStream_t stream) {
+    int most = 8;
+    if (sort_shape(p.n, 16).ctas > 8) {
+        const cudaError_t e = most_ctas<ID>(&most);
+        if (e != cudaSuccess) return e;
+    }
+    const SortShape shape = sort_shape(p.n, most);
+    return shape.keep ? launch_t<ID, true>(p, shape, stream) : launch_t<ID, false>(p, shape, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_sort(const SortParams& p, cudaStream_t stream) {
-    // CTAs: one per 1024 slots, up to 16 (4096 slots: 5.4 us, 6.5 with 2048 a CTA; 131072: 18 us, 30 with 8 CTAs)
-    int C = 1;
-    while (C < 16 && int64_t(p.n) > int64_t(C) * 1024) C *= 2;
-    const int64_t steps = (int64_t(p.n) + 31) / 32;
-    const int64_t per_cta = (steps + C - 1) / C * 32;  // slots of a CTA, at most
-    if (per_cta <= kMaxKeptSlots)
-        return p.ids64 ? launch_t<int64_t, true>(p, C, int32_t(per_cta), stream)
-                       : launch_t<int32_t, true>(p, C, int32_t(per_cta), stream);
-    return p.ids64 ? launch_t<int64_t, false>(p, C, 0, stream) : launch_t<int32_t, false>(p, C, 0, stream);
+    return p.ids64 ? launch_id<int64_t>(p, stream) : launch_id<int32_t>(p, stream);
 }
 
 }  // namespace moe
