@@ -126,3 +126,55 @@ def test_unnamed_rows_in_a_replayed_graph_and_beside_another_stream(cuda_device)
         for a, b in zip(got, beside):
             assert torch.equal(a, b) and torch.isfinite(a).all()
             assert torch.all(a[np.setdiff1d(np.arange(T * k), sr)] == 0.0)
+
+
+# ------------------------------------------------------------------ prompts
+
+# Enough tokens that every CTA of combine and of its gradient takes several: two slots of long 16-bit rows (128 threads a
+# token), three and eight slots, fp32, a row length that is not a multiple of 8, and one below 1024
+PROMPTS = [(2000, 2, 2048, "f16", "bf16"), (2500, 2, 4096, "bf16", "bf16"), (2000, 3, 1024, "bf16", "f32"),
+           (1300, 8, 512, "f16", "f16"), (3001, 2, 2048, "f32", "f32"), (3000, 2, 2051, "bf16", "f16"),
+           (2600, 3, 1027, "f32", "bf16"), (20011, 2, 136, "f16", "f16"), (21001, 5, 67, "bf16", "bf16")]
+
+
+def _half_step(ref, dt, slack):
+    mag = np.abs(ref) + slack
+    return slack + mag * (torch.finfo(DT[dt]).eps / 2) + (2.0 ** -25 if dt == "f16" else 2.0 ** -126)
+
+
+@pytest.mark.parametrize("T,k,H,dt,out", PROMPTS)
+@pytest.mark.parametrize("none,drop", [(0.0, 0.0), (0.05, 0.1)])
+def test_prompts(cuda_device, T, k, H, dt, out, none, drop):
+    v = _rows(T, k, H, none, drop).astype(np.int64)
+    slot_row = torch.from_numpy(v.astype(np.int32)).to(cuda_device)
+    g = torch.Generator().manual_seed(T)
+    y = torch.randn(T * k, H, generator=g).to(DT[dt])
+    w = torch.rand(T, k, generator=g)
+    d = torch.randn(T, H, generator=g).to(DT[out])
+    yd, wd, dd = y.to(cuda_device), w.to(cuda_device), d.to(cuda_device)
+    got = bgq.moe_combine(yd, wd, slot_row, out=out).cpu().double().numpy()
+    back = bgq.moe_dispatch_backward(yd, slot_row).cpu().double().numpy()
+    d_y, d_w = (t.cpu().double().numpy() for t in bgq.moe_combine_backward(dd, yd, wd, slot_row))
+    x_r = bgq.moe_dispatch(dd, slot_row).cpu()
+    yh, wh, dh = y.double().numpy(), w.double().numpy(), d.double().numpy()
+    kept = v >= 0
+    ref_y, ref_x = np.zeros((T * k, H)), torch.zeros(T * k, H, dtype=DT[out])
+    t, s = np.nonzero(kept)
+    ref_y[v[kept]] = wh[t, s, None] * dh[t]
+    ref_x[v[kept]] = d[t]
+    assert torch.equal(x_r, ref_x)
+    assert np.all(np.abs(d_y - ref_y) <= _half_step(ref_y, dt, 2.0 ** -24 * np.abs(ref_y)))
+    comb, comb_mag, plain, plain_mag = np.zeros((4, T, H))
+    for i in range(k):
+        rows = np.where(kept[:, i, None], yh[np.maximum(v[:, i], 0)], 0.0)
+        comb += wh[:, i, None] * rows
+        comb_mag += np.abs(wh[:, i, None] * rows)
+        plain += rows
+        plain_mag += np.abs(rows)
+        prod = rows * dh
+        # chains of at least H / 32 products (and 8 more of a vector), then 13 tree steps
+        assert np.all(np.abs(d_w[:, i] - prod.sum(1)) <= (H / 32 + 8 + 13 + 1) * 2.0 ** -24 * np.abs(prod).sum(1))
+    assert np.all(d_w[~kept] == 0.0)
+    assert np.all(np.abs(got - comb) <= _half_step(comb, out, k * 2.0 ** -24 * comb_mag))
+    assert np.all(np.abs(back - plain) <= _half_step(plain, dt, k * 2.0 ** -24 * plain_mag))
+    assert bgq.device_status() == 0
