@@ -854,8 +854,10 @@ def w4a16_gemv_grouped(x: torch.Tensor, row_index: torch.Tensor | None, expert_o
     themselves (row_index None); expert_offsets [E+1] int64 on the device, its
     last value at most R; packed and s_g (or S with alpha): lists of per-expert
     tensors (None for experts without rows) or int64 CUDA tensors of device
-    pointers (then N is needed); out_row [R] int32: the output row of each
-    routed row (None: row i).  Rows of y that nothing names are not written."""
+    pointers (device_pointers, once beside the weights; then N is needed.  A list
+    is copied to the device in every call, which a CUDA graph cannot capture);
+    out_row [R] int32: the output row of each routed row (None: row i), of y_rows
+    rows (R unless given).  Rows of y that nothing names are not written."""
     dt, ld = _float_rows("x", x)
     if row_index is not None:
         _need_cuda("row_index", row_index, torch.int32, 1)
