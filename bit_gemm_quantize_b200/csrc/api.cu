@@ -349,7 +349,12 @@ w4a8::w4a16::Params w4a16_params(const void* x, int64_t x_rows, int64_t ldx, int
     p.group_magic = group == 128 ? 0u : uint32_t((uint64_t(1) << 32) / uint64_t(group / 128)) + 1u;
     p.x_type = x_elem;
     p.y_type = y_elem;
-    p.out_scale = 256.0f / float(alpha > 0 ? alpha : 1);
+    // with integer scales up to 2^15 the sums are alpha times the outputs: what 2^8 does not
+    // take off is taken off the tokens, so that no sum overflows where its output would not
+    // (2: the high pair of digits alone may round up to twice a power of two)
+    const float scale = 256.0f / float(alpha > 0 ? alpha : 1);
+    p.out_scale = scale > 2.0f ? scale : 2.0f;
+    p.x_scale = scale / p.out_scale;
     p.status = status;
     return p;
 }

@@ -18,7 +18,7 @@
 // largest magnitude.  fp16 and bf16 values that are at least 2^-19 or 2^-22 of
 // the block's largest, and fp32 values at least 2^-6 of it, are kept exactly; an
 // fp32 sum of the products would round at 2^-24 of the largest one.  (Blocks whose
-// largest value is below 2^-108 keep fewer bits.)  The cut is relative to the largest
+// largest value is below 2^-108, or 2^-115 alpha, keep fewer bits.)  The cut is relative to the largest
 // value, also where a code of 0 keeps that one out of the product: a token with a
 // block of a few large values over much smaller ones is multiplied again in fp32
 // (few_large, plain_runs), so that elsewhere a cut is within 2^-20 of the largest of
@@ -182,7 +182,8 @@ __device__ __forceinline__ bool few_large(float v0, float v1, float v2, float v3
 // 4 h + 3.  Returns the factors of the low and the high pair of digits, which
 // include 1/16 for the 16 q of the weights and 2^-8, so that a value next to the
 // largest fp32 one does not overflow where its high pair rounds up (the output
-// step multiplies by 2^8).  Sets `plain` where the block is not for digits.
+// step multiplies by 2^8; with integer scales it is a part of 2^8 / alpha, and the
+// caller multiplies the factors by the other).  Sets `plain` where the block is not for digits.
 __device__ __forceinline__ float2 block_digits(const float (&v)[8], int type, uint32_t (&dig)[4][2],
                                                bool& plain) {
     uint32_t top = 0u;
@@ -250,7 +251,7 @@ struct Run {
 // (token, block) pairs per warp step, 16 lanes each; lane (xt, xw) of a pair has
 // the 8 values that word xw of the weights of lanes t = xt meets.
 __device__ __noinline__ void stage_tokens(const void* x, int type, int64_t ldx, Rows& rows, int m_rows, int kb0,
-                                          int kb1, uint4* xs, float2* fs) {
+                                          int kb1, float scale, uint4* xs, float2* fs) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int xt = lane & 3, xh = (lane >> 2) & 1, xw = lane >> 3;
     const uint32_t pairs = uint32_t(m_rows * (kb1 - kb0));
@@ -268,7 +269,7 @@ __device__ __noinline__ void stage_tokens(const void* x, int type, int64_t ldx, 
             uint2* dst = reinterpret_cast<uint2*>(xs + ((kb * 2 + (xw >> 1)) * m_rows + m) * 16 + xt) + (xw & 1);
 #pragma unroll
             for (int d = 0; d < 4; ++d) dst[d * 8] = make_uint2(dig[d][0], dig[d][1]);
-            if (xt == 0 && xw == 0) fs[q] = F;
+            if (xt == 0 && xw == 0) fs[q] = make_float2(F.x * scale, F.y * scale);
         }
     }
 }
@@ -342,6 +343,7 @@ template <bool INT>
 __device__ __forceinline__ void plain_tokens(const Params& p, const Run& run, const Rows& rows, uint32_t tokens) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int C = 1 << p.cluster_log, rank = int(blockIdx.x) & (C - 1);
+    const float scale = 0x1p-8f * p.x_scale;  // as in the factors
     for (; tokens; tokens &= tokens - 1) {
         const int m = __ffs(int(tokens)) - 1;
         const int64_t xrow = rows.src[m] * p.ldx;
@@ -352,7 +354,7 @@ __device__ __forceinline__ void plain_tokens(const Params& p, const Run& run, co
                 float v[8];
                 load_tokens(p.x, p.x_type, xrow + k0, v);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) v[j] *= 0x1p-8f;  // as in the factors
+                for (int j = 0; j < 8; ++j) v[j] *= scale;
                 const int kb = k0 >> 7;
                 const int64_t at = int64_t(p.group_magic ? int(__umulhi(uint32_t(kb), p.group_magic)) : kb) * p.N + n;
 #pragma unroll
@@ -491,7 +493,7 @@ __device__ __forceinline__ void run_columns(const Params& p, const Run& run, Row
 
             if (panels > 1 || b0 == run.col0) {
                 __syncthreads();  // the rows are set; the last panel's tokens have been used
-                stage_tokens(p.x, p.x_type, p.ldx, rows, m_rows, kb0, kb1, xs, fs);
+                stage_tokens(p.x, p.x_type, p.ldx, rows, m_rows, kb0, kb1, p.x_scale, xs, fs);
             }
             __syncthreads();
 

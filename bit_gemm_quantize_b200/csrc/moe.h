@@ -85,7 +85,9 @@ struct Params {
     int32_t E, N, K;
     uint32_t group_magic;            // block kb's group: umulhi(kb, magic), or kb when 0
     int32_t x_type, y_type;          // ElemType
-    float out_scale;                 // 2^8, over alpha for integer scales
+    // 2^8, or 2^8 / alpha for integer scales, in two parts: 1 or less for the tokens,
+    // 2 or more for the sums
+    float x_scale, out_scale;
     int* status;
     // set by launch(): log2 of the CTAs along K and of the warps along a CTA's
     // part, bytes of shared memory for the tokens, whether that takes panels of

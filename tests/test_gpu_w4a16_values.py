@@ -163,3 +163,64 @@ def test_large_values_over_zero_codes(cuda_device, form, kind, dt, ratio, outlie
         mag = _definition(x, q, scale, kind)[1]
         _same(y, ref, mag, _chain(K))
     assert bgq.device_status() == 0
+
+
+def _in_groups(x, M):
+    return [x[i:i + M] for i in range(0, x.shape[0], M)]
+
+
+@pytest.mark.parametrize("form", ["dense", "experts"])
+@pytest.mark.parametrize("M", TOKENS)
+@pytest.mark.parametrize("kind,alpha", [("float", 1), ("int", 1), ("int", 256), ("int", 1024), ("int", 1 << 14),
+                                        ("int", 1 << 22)])
+def test_single_values_over_the_exponent_range(cuda_device, form, M, kind, alpha):
+    """One value at a time over codes of 1 and a scale that is a power of two: the value times the scale, to the last
+    bit, from the largest fp32 value down to 2^-100 (or as far as the integers reach)."""
+    K, N = 256, 16
+    rng = np.random.default_rng(M)
+    S = min(alpha, 1 << 14)
+    low = max(-100, -115 + int(np.log2(alpha)))
+    vals = np.ldexp(rng.uniform(1, 2, 24).astype(np.float32), rng.integers(low, 127, 24)).astype(np.float32)
+    vals = np.concatenate([vals, -vals, np.float32([np.finfo(np.float32).max, -np.finfo(np.float32).max, 2.0 ** low, 0.0])])
+    x = np.zeros((vals.size, K), np.float32)
+    x[np.arange(vals.size), np.arange(vals.size) * 5 % K] = vals
+    scale = np.full((2, N), 1.0 if kind == "float" else S)
+    want = vals * np.float32(S / alpha)
+    y = torch.cat([_call(form, part, np.ones((N, K), np.int64), scale, kind, alpha=alpha)
+                   for part in _in_groups(torch.from_numpy(x).to(cuda_device), M)])
+    assert np.array_equal(y.cpu().numpy(), np.repeat(want[:, None], N, axis=1))
+
+
+@pytest.mark.parametrize("form", ["dense", "experts"])
+@pytest.mark.parametrize("M", TOKENS)
+@pytest.mark.parametrize("kind", ["float", "int"])
+@pytest.mark.parametrize("dt", ["f16", "bf16", "f32"])
+def test_every_place_and_code(cuda_device, form, M, kind, dt):
+    """Unit tokens read the weights back exactly: every code, every place of the packed word, every token of a pass."""
+    K, N = 256, 40
+    rng = np.random.default_rng(M)
+    q = rng.integers(-8, 8, (N, K))
+    scale = rng.integers(1, 9, (K // 128, N))
+    eye = torch.eye(K)[rng.permutation(K)[:66]]
+    y = torch.cat([_call(form, part, q, scale, kind, alpha=1) for part in _in_groups(eye.to(DT[dt]).to(cuda_device), M)])
+    w = q * np.repeat(scale.T, 128, axis=1)
+    assert np.array_equal(y.cpu().numpy(), eye.numpy().astype(np.float64) @ w.T)
+
+
+@pytest.mark.parametrize("form", ["dense", "experts"])
+@pytest.mark.parametrize("M", TOKENS)
+@pytest.mark.parametrize("kind", ["float", "int"])
+@pytest.mark.parametrize("dt", ["f16", "bf16", "f32"])
+def test_every_value_keeps_its_bits(cuda_device, form, M, kind, dt):
+    """Columns with a single code: each value of a token comes back on its own, off by at most 2^-30 of the largest of
+    its block (in no unit of sums, so that the lowest digit counts), in a pass of every number of tokens."""
+    K, N = 384, 384
+    rng = np.random.default_rng(M)
+    x = rng.standard_normal((M, K)) * 2.0 ** rng.integers(-8, 9, (M, 3)).repeat(128, axis=1)
+    x[:, 5::61] *= 30.0
+    x = torch.from_numpy(x.astype(np.float32)).to(DT[dt]).to(cuda_device)
+    code = rng.permutation([1, 2, 4, -1, -2, -4, -8] * 55)[:N]
+    y = _call(form, x, np.diag(code), np.ones((3, N)), kind, alpha=1).double().cpu().numpy()
+    xh = x.double().cpu().numpy()
+    top = np.abs(xh).reshape(M, 3, 128).max(2).repeat(128, axis=1)
+    assert np.all(np.abs(y - xh * code) <= 2.0 ** -30 * top * np.abs(code))
