@@ -10,8 +10,8 @@
 // nothing is accumulated through memory: sums are fp32, in slot order, rounded
 // once.  No atomics.
 //
-// Measured at the copy rate's share (2 slots, rows of 8 KB): dispatch 84 %, combine
-// 79 %, its gradient 89 %; rows of odd lengths reach 35 to 60 %.
+// Measured at the copy rate's share (2 slots, rows of 8 KB): dispatch 85 %, combine
+// 79 %, its gradient 90 %; rows of odd lengths reach 35 to 60 %.
 //
 // What they need is enough loads in flight: a token's kSlots slots (2 or 4, as
 // top_k has) are looked up together, then the loads of all of them go out, U
@@ -449,22 +449,31 @@ cudaError_t combine_e(const RowParams& p, int num_sms, cudaStream_t stream) {
     return cudaLaunchKernelEx(&lc.cfg, kern, p, s.tpt_log, s.chunks, s.items);
 }
 
+// Two slots of many long 16-bit rows take 128 threads a token with two pieces of each
+// slot in flight, else 256 threads and one.  The rule, measured at 150 to 8192 tokens and
+// rows of 1024 to 14336 (148 SMs): combine gains 2 to 14 % from 1600 tokens of 2048 on
+// (4096 tokens of 4096: 20.5 us against 21.9) and loses 1 to 11 % at 592 and 1200 (1200
+// of 8192: 15.8 against 14.2); rows of 1024 lose 21 %.  The gradient gains 2 to 10 % up to
+// rows of 4096 (4096 tokens: 29.4 against 30.6) and loses 1 to 7 % with longer ones
+// (8192 tokens of 8192: 114 against 107).  fp32 rows and more slots lose by it (18.7
+// against 18.4, 20.9 against 19.6).
+bool many_long_rows(const RowParams& p, size_t elem_bytes, int num_sms) {
+    return elem_bytes == 2 && p.top_k <= 2 && p.H >= 2048 && p.T >= 10 * int64_t(num_sms);
+}
+
 // Rows in 16-byte pieces of 8 elements (both types): lengths a multiple of 8,
-// bases and strides 16-byte aligned.  Two slots of many long 16-bit rows take 128
-// threads a token with two pieces of each slot in flight (4096 tokens, 2 slots,
-// rows of 8 KB: 19.5 us against 21.1 with 256 threads and one piece; fp32 rows
-// and more slots lose by it: 18.7 against 18.4, 20.9 against 19.6).  Otherwise
-// one element at a time, with the threads per token (32 or 256) known at compile
-// time: the pieces of a thread are then constant distances apart, which halves
-// the registers (2048 tokens, 2 slots, 4095 bf16: 15.8 us against 22.0).
+// bases and strides 16-byte aligned.  Otherwise one element at a time, with the
+// threads per token (32 or 256) known at compile time: the pieces of a thread are then
+// constant distances apart, which halves the registers (2048 tokens, 2 slots, 4095
+// bf16: 15.8 us against 22.0).
 template <typename TY, typename TO>
 cudaError_t combine_t(const RowParams& p, int num_sms, cudaStream_t stream) {
     const bool two = p.top_k <= 2, shorter = p.H < 1024;
-    const bool many = two && p.H >= 2048 && p.T >= 4 * num_sms;
+    const bool many = many_long_rows(p, sizeof(TY), num_sms);
     if (p.H % 8 == 0 && aligned(p.a) && aligned(p.out) && p.lda * int64_t(sizeof(TY)) % 16 == 0)
-        return many && sizeof(TY) == 2 ? combine_e<TY, TO, 8, 2, 2, 7>(p, num_sms, stream)
-               : two                   ? combine_e<TY, TO, 8, 1, 2, 0>(p, num_sms, stream)
-                                       : combine_e<TY, TO, 8, 1, 4, 0>(p, num_sms, stream);
+        return many  ? combine_e<TY, TO, 8, 2, 2, 7>(p, num_sms, stream)
+               : two ? combine_e<TY, TO, 8, 1, 2, 0>(p, num_sms, stream)
+                     : combine_e<TY, TO, 8, 1, 4, 0>(p, num_sms, stream);
     if (shorter)
         return two ? combine_e<TY, TO, 1, 8, 2, 5>(p, num_sms, stream) : combine_e<TY, TO, 1, 4, 4, 5>(p, num_sms, stream);
     return two ? combine_e<TY, TO, 1, 8, 2, 8>(p, num_sms, stream) : combine_e<TY, TO, 1, 4, 4, 8>(p, num_sms, stream);
@@ -487,12 +496,12 @@ cudaError_t backward_e(const RowParams& p, int num_sms, cudaStream_t stream) {
 template <typename TD, typename TY>
 cudaError_t backward_t(const RowParams& p, int num_sms, cudaStream_t stream) {
     const bool two = p.top_k <= 2, shorter = p.H < 1024;
-    const bool many = two && p.H >= 2048 && p.T >= 4 * num_sms;
+    const bool many = many_long_rows(p, sizeof(TY), num_sms) && p.H <= 4096;
     if (p.H % 8 == 0 && aligned(p.a) && aligned(p.b) && aligned(p.out) && p.lda * int64_t(sizeof(TD)) % 16 == 0 &&
         p.ldb * int64_t(sizeof(TY)) % 16 == 0)
-        return many && sizeof(TY) == 2 ? backward_e<TD, TY, 8, 2, 2, 7>(p, num_sms, stream)
-               : two                   ? backward_e<TD, TY, 8, 1, 2, 0>(p, num_sms, stream)
-                                       : backward_e<TD, TY, 8, 1, 4, 0>(p, num_sms, stream);
+        return many  ? backward_e<TD, TY, 8, 2, 2, 7>(p, num_sms, stream)
+               : two ? backward_e<TD, TY, 8, 1, 2, 0>(p, num_sms, stream)
+                     : backward_e<TD, TY, 8, 1, 4, 0>(p, num_sms, stream);
     if (shorter)
         return two ? backward_e<TD, TY, 1, 4, 2, 5>(p, num_sms, stream) : backward_e<TD, TY, 1, 4, 4, 5>(p, num_sms, stream);
     return two ? backward_e<TD, TY, 1, 4, 2, 8>(p, num_sms, stream) : backward_e<TD, TY, 1, 4, 4, 8>(p, num_sms, stream);
