@@ -224,3 +224,89 @@ def test_every_value_keeps_its_bits(cuda_device, form, M, kind, dt):
     xh = x.double().cpu().numpy()
     top = np.abs(xh).reshape(M, 3, 128).max(2).repeat(128, axis=1)
     assert np.all(np.abs(y - xh * code) <= 2.0 ** -30 * top * np.abs(code))
+
+
+@pytest.mark.parametrize("M,K,N", [(1301, 256, 24), (700, 2048, 40), (333, 4096, 16)])
+@pytest.mark.parametrize("kind", ["float", "int"])
+def test_infinities_among_many_tokens(cuda_device, M, K, N, kind):
+    """More passes than clusters, so that each takes several: some with tokens that are multiplied in fp32, some not."""
+    rng = np.random.default_rng(M)
+    x = rng.standard_normal((M, K)).astype(np.float32)
+    for m in rng.permutation(M)[:M // 7]:
+        x[m, rng.integers(K, size=2)] = rng.choice([-np.inf, np.inf], 2)
+    q = rng.integers(-8, 8, (N, K))
+    scale = _scales(rng, K, N, kind)
+    x = torch.from_numpy(x).to(cuda_device)
+    y = _call("dense", x, q, scale, kind)
+    ref, mag = _definition(x, q, scale, kind)
+    _same(y, ref, mag, _chain(K), _block_slack(x, q, scale, kind))
+    clean = torch.isfinite(x).all(1)
+    other = torch.where(clean[:, None], x, torch.zeros_like(x))  # the tokens beside them are as without them
+    assert torch.equal(y[clean], _call("dense", other, q, scale, kind)[clean])
+
+
+@pytest.mark.parametrize("T,k,E,K,N", [(400, 2, 200, 256, 24), (16, 2, 8, 4096, 264), (90, 3, 5, 1408, 40)])
+@pytest.mark.parametrize("kind", ["float", "int"])
+def test_infinities_among_experts(cuda_device, T, k, E, K, N, kind):
+    """Every expert its own weights, dropped slots, outputs in slot order: infinities in some tokens, and blocks of a few
+    large values over zero codes in others."""
+    rng = np.random.default_rng(T)
+    x = rng.standard_normal((T, K)).astype(np.float32)
+    x[::5, 7], x[::5, 100] = np.inf, -np.inf
+    x[1::5, 128:256] *= 1e-4
+    x[1::5, 131] = 2e4
+    x = torch.from_numpy(x).to(cuda_device)
+    ids = np.stack([rng.permutation(E)[:k] for _ in range(T)])
+    ids[rng.random((T, k)) < 0.1] = -1
+    r = bgq.moe_route_sort(torch.from_numpy(ids).to(cuda_device), E)
+    qs = [rng.integers(-8, 8, (N, K)) for _ in range(E)]
+    for q in qs:
+        q[:, 131] = 0
+    scales = [_scales(rng, K, N, kind) for _ in range(E)]
+    packed = [_pack(q).to(cuda_device) for q in qs]
+    s = [torch.from_numpy(v.astype(np.float32 if kind == "float" else np.int16)).to(cuda_device) for v in scales]
+    kw = dict(s_g=s) if kind == "float" else dict(S=s, alpha=1024)
+    y = torch.full((T * k, N), 5.0, device=cuda_device)
+    bgq.w4a16_gemv_grouped(x, r["row_index"], r["expert_offsets"], packed, out="f32", y=y, out_row=r["out_row"], **kw)
+    y = y.reshape(T, k, N)
+    for e in range(E):
+        t, slot = np.nonzero(ids == e)
+        if t.size:
+            xe = x[torch.from_numpy(t).to(cuda_device)]
+            ref, mag = _definition(xe, qs[e], scales[e], kind)
+            slack = _block_slack(xe, qs[e], scales[e], kind)
+            slack[t % 5 == 1] = 0.0  # multiplied in fp32
+            _same(y[torch.from_numpy(t).to(cuda_device), torch.from_numpy(slot).to(cuda_device)], ref, mag, _chain(K), slack)
+    assert torch.all(y[torch.from_numpy(ids < 0).to(cuda_device)] == 5.0)
+    assert bgq.device_status() == 0
+
+
+def test_graph_and_streams_with_tokens_in_fp32(cuda_device):
+    """A captured call whose tokens hold infinities in some replays and not in others, beside calls on another stream."""
+    rng = np.random.default_rng(0)
+    K, N, M = 2048, 520, 5
+    q, scale = rng.integers(-8, 8, (N, K)), _scales(rng, K, N, "float")
+    clean = torch.from_numpy(rng.standard_normal((M, K)).astype(np.float32)).to(cuda_device)
+    bad = clean.clone()
+    bad[3, 11], bad[0, 2000] = float("inf"), float("-inf")
+    want = [_call("dense", v, q, scale, "float") for v in (clean, bad)]
+    assert torch.equal(torch.isnan(want[1][3]), torch.from_numpy(q[:, 11] == 0).to(cuda_device))
+    packed, s = _pack(q).to(cuda_device), torch.from_numpy(scale).to(cuda_device)
+    x = clean.clone()
+    call = lambda v: bgq.w4a16_gemv(v, packed, s_g=s, out="f32")
+    call(x)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = call(x)
+    other = torch.cuda.Stream()
+    for i in (1, 0, 1, 1, 0):
+        x.copy_((clean, bad)[i])
+        torch.cuda.synchronize()
+        graph.replay()
+        with torch.cuda.stream(other):
+            beside = call((clean, bad)[1 - i])
+        torch.cuda.synchronize()
+        for got, ref in ((y, want[i]), (beside, want[1 - i])):
+            assert torch.equal(torch.nan_to_num(got, nan=7.0), torch.nan_to_num(ref, nan=7.0))
+            assert torch.equal(torch.isnan(got), torch.isnan(ref))
