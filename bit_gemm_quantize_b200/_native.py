@@ -602,6 +602,8 @@ def w4a8_gemm_intscale_grouped(q_x, s_a, row_index, expert_offsets, packed, S, a
 
 
 # ------------------------------------------------------------------ mixture-of-experts rows and W4A16 products
+# Plain functions: no call records a gradient, and a result of tensors that require one
+# is detached from them.  The gradients have calls of their own.
 
 _FLOAT = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
 _FLOAT_OUT = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
@@ -633,7 +635,9 @@ def _address(t):
 def _launch(name, dev, *args):
     """Call a library entry on the current stream (its last argument) of device
     number dev, with that the current device.  Short, because a decode step's
-    small kernels take less time than their calls."""
+    small kernels take less time than their calls (so the device and the stream's
+    handle are read where torch's compiled code reads them: torch.cuda's calls
+    make an object each time)."""
     fn = getattr(_lib or load(), name)
     if torch._C._cuda_getDevice() == dev:
         code = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
@@ -704,8 +708,8 @@ def moe_dispatch(x: torch.Tensor, slot_row: torch.Tensor, *, x_r: torch.Tensor |
     """Token rows x [T, H] (fp32, fp16 or bf16) in expert order: x_r[slot_row[t, s]]
     = x[t]; the rows of dropped slots are zeroed.  x_r [T*top_k, H] unless given
     (more rows may be).  Rows that no slot names (a slot of -1 names none) are zero in
-    a result allocated here and stay as they were in a given one.  Its gradient is
-    moe_dispatch_backward."""
+    a result allocated here and stay as they were in a given one.  x_r is detached
+    from x; the gradient is moe_dispatch_backward."""
     dt, ld = _float_rows("x", x)
     _need_cuda("slot_row", slot_row, torch.int32, 2)
     T, H = x.shape
@@ -757,7 +761,9 @@ def moe_combine(y: torch.Tensor, weights: torch.Tensor | None, slot_row: torch.T
     [T, H] with row t = sum_s weights[t, s] * y[slot_row[t, s]] (fp32 sum in slot
     order; dropped slots add nothing).  slot_row None: slot f's output is row f
     (written through out_row; not after dropped slots, whose rows nothing
-    wrote); weights None: ones (then slot_row or top_k gives the slots).  out: 'f16', 'bf16' or 'f32', y's type unless given."""
+    wrote); weights None: ones (then slot_row or top_k gives the slots).  out: 'f16',
+    'bf16' or 'f32', y's type unless given.  The result is detached from y and
+    weights; their gradients are moe_combine_backward."""
     if weights is not None:
         _need_cuda("weights", weights, torch.float32, 2)
     return _combine(y, weights, slot_row, top_k, out, result)
@@ -808,7 +814,7 @@ def w4a16_gemv(x: torch.Tensor, w_packed: torch.Tensor, *, s_g: torch.Tensor | N
     """y [M, N] = unquantized tokens x [M, K] (fp32, fp16 or bf16) times the
     packed 4-bit weights, with float group scales s_g or integer ones S / alpha
     (out: 'f16', 'bf16' or 'f32').  For decode: one pass over the weights serves
-    8 tokens."""
+    8 tokens.  y carries no gradient."""
     dt, ld = _float_rows("x", x)
     _need_cuda("w_packed", w_packed, torch.uint8, 2)
     _one_scale(s_g, S, alpha)
@@ -857,7 +863,8 @@ def w4a16_gemv_grouped(x: torch.Tensor, row_index: torch.Tensor | None, expert_o
     pointers (device_pointers, once beside the weights; then N is needed.  A list
     is copied to the device in every call, which a CUDA graph cannot capture);
     out_row [R] int32: the output row of each routed row (None: row i), of y_rows
-    rows (R unless given).  Rows of y that nothing names are not written."""
+    rows (R unless given).  Rows of y that nothing names are not written.  y carries
+    no gradient."""
     dt, ld = _float_rows("x", x)
     if row_index is not None:
         _need_cuda("row_index", row_index, torch.int32, 1)

@@ -61,11 +61,11 @@
 // staged in panels, with the columns' sums kept in shared memory between them.
 //
 // Measured (in a row, weights from HBM): K = 4096, N = 22016: one token 12.2 us
-// (7.4 us of HBM at the copy rate and 2.9 us that an empty launch of this shape
-// takes), 3 tokens 15.0, 8 tokens 21.5 (bound by instruction issue); K = 11008,
-// N = 4096, 8 tokens 18.5; two of eight experts of K = 4096, N = 14336 for one
-// token 16.5 (9.4 of HBM), all eight for 16 tokens 56 (39).  Two CTAs of 8 warps
-// on an SM were slower (13.7 us at one token).
+// (7.4 us of HBM at the copy rate; the first weights are requested only after the
+// previous kernel has ended), 3 tokens 14.9, 8 tokens 20.9 to 22.3, 16 tokens (two
+// passes) 36; K = 11008, N = 4096, 8 tokens 18.8; two of eight experts of K = 4096,
+// N = 14336 for one token 16.4 (9.4 of HBM), all eight for 16 tokens 50 to 59 as the
+// routing has it (39).  Two CTAs of 8 warps on an SM were slower (13.7 us at one token).
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -724,7 +724,9 @@ __device__ __noinline__ void plain_runs(const Params& p, Tables<GROUPED>& tab) {
 }
 
 // One kernel for each number of token tiles: together, three bodies share one
-// register allocation and spill (8 tokens 25 -> 28 us).
+// register allocation and spill more (8 tokens 25 -> 28 us; alone, the forms for 3 and 4
+// tokens spill up to 56 bytes, the one of one or two tokens per expert 4, the others
+// nothing).
 template <int NT, bool INT, bool GROUPED>
 __global__ void __launch_bounds__(kThreads, 1) w4a16_kernel(const __grid_constant__ Params p) {
     constexpr uint32_t kRows = rows_of(NT);
@@ -883,9 +885,9 @@ cudaError_t launch_t(Params& p, int num_sms, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     // CTAs that split K: so many that making the tokens' digits stays short, 128
     // (token, block) pairs in a CTA (64 where a pass of 8 tokens is bound by its
-    // arithmetic).  K = 11008, N = 4096, 8 tokens: 39 us with one CTA, 20 with 8;
-    // K = 4096, N = 22016: 3 tokens 15.1 with one, 15.7 with 2; 8 tokens 32 with
-    // one, 24.8 with 2, 21.5 with 4.
+    // arithmetic).  K = 11008, N = 4096, 8 tokens: 39.8 us with one CTA, 28.7 with 2,
+    // 21.2 with 4, 18.8 with 8; K = 4096, N = 22016: 3 tokens 14.8 with one, 15.7 with 2;
+    // 8 tokens 32.2 with one, 22.3 with 2, 20.9 with 4.
     const int nkb = p.K / 128;
     p.max_rows = int(p.R < kRows ? p.R : kRows);
     p.cluster_log = 0;
@@ -903,7 +905,7 @@ cudaError_t launch_t(Params& p, int num_sms, cudaStream_t stream) {
     // the others side by side on tiles of their own.  Fewer warps along K let the
     // sums meet less often: in a cluster at least two blocks a warp, and elsewhere
     // as few as leave six steps (16 tokens, 2 of 8 experts each, K = 4096,
-    // N = 14336: 56.5 us with 4 warps, 63 with 16).
+    // N = 14336: 56.3 us with 4 warps, 62.3 with 16).
     p.ks_log = 4;
     while (p.ks_log > 0 && (1 << (p.ks_log - 1)) >= part) --p.ks_log;
     while (p.ks_log > 0 && (part >> p.ks_log) < 2 && p.cluster_log) --p.ks_log;
@@ -952,7 +954,7 @@ cudaError_t launch(Params p, bool scale_int, int num_sms, cudaStream_t stream) {
     // Tokens of a pass: up to 2, 4 or 8, as there are.  An expert's rows are not
     // known here: up to 1.5 or 4.5 an expert on average, passes of 2 or 4 (some
     // experts then take a second one, from L2) beat emptier ones of twice as many
-    // (16 tokens, 2 of 8 experts each, K = 4096, N = 14336: 62 us against 84).
+    // (16 tokens, 2 of 8 experts each, K = 4096, N = 14336: 56 us against 94).
     const int64_t live = p.offsets ? (p.E < p.R ? p.E : p.R) : 1;
     if (p.R <= 2 || 2 * p.R <= 3 * live) return launch_nt<1>(p, scale_int, num_sms, stream);
     if (p.R <= 4 || 2 * p.R <= 9 * live) return launch_nt<2>(p, scale_int, num_sms, stream);
