@@ -130,58 +130,72 @@ __device__ __forceinline__ int32_t slot_target(const RowParams& p, int32_t f) {
 
 // Rows that no slot names (a slot of -1, or a row outside, leaves one) are known only
 // when all slots have been seen.  Where the caller wants them cleared, the grid's
-// first CTAs do it beside the others, each for kClearRows rows: it counts the rows that
-// are named, and unless all are, marks those among its own and clears the rest.  The
+// first CTAs look for them beside the others' work, one CTA for 1024 rows and a share
+// of the slots.  While every slot of its share names a row that is all it does: with
+// R <= T * top_k distinct rows, one without a slot means a slot without one.  The CTAs
+// that find such a slot see by another look at all slots which others do, and share
+// the rows: each marks those of its part that are named and clears the rest.  The
 // others write named rows only, so nothing has to wait.  (Clearing the whole output
 // first would cost a third of a dispatch: 2048 tokens, 2 slots, 8 KB rows.)
-constexpr int kClearRows = 1024;
+constexpr int kClearRows = 1024, kMaxClears = 1024;  // rows of a CTA, CTAs
+constexpr int kMarkedRows = 16384;                   // rows marked at a time, at most
 
 unsigned clear_ctas(const RowParams& p) {
     // without slot_row every row of R <= T * top_k is named
-    return p.zeroed && p.slot_row ? unsigned((p.R + kClearRows - 1) / kClearRows) : 0u;
+    if (!p.zeroed || !p.slot_row) return 0u;
+    const int64_t n = (p.R + kClearRows - 1) / kClearRows;
+    return unsigned(n < kMaxClears ? n : kMaxClears);
 }
 
-// f(the row that a slot names, 2^31 or more for none), for every slot of this thread.
-template <typename F>
-__device__ __forceinline__ void each_row(const int32_t* slot_row, int32_t n, F&& f) {
-    const auto row = [](int32_t v) { return uint32_t(v >= 0 ? v : -2 - v); };
-    int32_t i = 0;
-    if ((reinterpret_cast<uintptr_t>(slot_row) & 15u) == 0) {
-#pragma unroll 4
-        for (int32_t q = threadIdx.x; q < n / 4; q += kThreads) {
-            const int4 v = __ldg(reinterpret_cast<const int4*>(slot_row) + q);
-            f(row(v.x)), f(row(v.y)), f(row(v.z)), f(row(v.w));
-        }
-        i = n / 4 * 4;
-    }
-    for (i += int32_t(threadIdx.x); i < n; i += kThreads) f(row(__ldg(slot_row + i)));
-}
+// The row that a slot of this value names, 2^31 or more for none.
+__device__ __forceinline__ uint32_t named_row(int32_t v) { return uint32_t(v >= 0 ? v : -2 - v); }
 
 template <typename V>
-__device__ __noinline__ void clear_unnamed(const int32_t* slot_row, int32_t n, uint32_t R, V* out, int32_t row_len) {
-    __shared__ uint32_t named[kClearRows / 32];
-    __shared__ uint32_t count;
-    if (threadIdx.x < kClearRows / 32) named[threadIdx.x] = 0u;
-    if (threadIdx.x == 0) count = 0u;
+__device__ __noinline__ void clear_unnamed(const int32_t* slot_row, int32_t n, uint32_t R, uint32_t clears, V* out,
+                                           int32_t row_len) {
+    __shared__ uint32_t named[kMarkedRows / 32];
+    __shared__ uint32_t parts[kMaxClears / 32];  // the shares that have a slot without a row
+    const uint32_t share = (uint32_t(n) + clears - 1) / clears, own = blockIdx.x * share;
+    bool missing = false;
+#pragma unroll 4
+    for (uint32_t i = threadIdx.x; i < share; i += kThreads)
+        if (own + i < uint32_t(n)) missing |= named_row(__ldg(slot_row + own + i)) >= R;
+    if (!__syncthreads_or(missing)) return;
+    if (threadIdx.x < kMaxClears / 32) parts[threadIdx.x] = 0u;
     __syncthreads();
-    uint32_t mine = 0u;
-    each_row(slot_row, n, [&](uint32_t r) { mine += r < R; });
-    mine = __reduce_add_sync(0xffffffffu, mine);
-    if ((threadIdx.x & 31) == 0) atomicAdd(&count, mine);
-    __syncthreads();
-    if (count >= R) return;
-    const uint32_t first = blockIdx.x * uint32_t(kClearRows), rows = min(R - first, uint32_t(kClearRows));
-    each_row(slot_row, n, [&](uint32_t r) {
-        if (r - first < rows) atomicOr(&named[(r - first) >> 5], 1u << ((r - first) & 31u));
-    });
-    __syncthreads();
-    for (uint32_t k = 0; k < rows; k += 32) {
-        uint32_t left = ~named[k >> 5];
-        if (rows - k < 32u) left &= (1u << (rows - k)) - 1u;
-        for (; left; left &= left - 1u) {
-            V* row = out + (int64_t(first + k) + __ffs(int(left)) - 1) * row_len;
-            for (int32_t c = threadIdx.x; c < row_len; c += kThreads) row[c] = V{};
+#pragma unroll 4
+    for (int32_t i = threadIdx.x; i < n; i += kThreads)
+        if (named_row(__ldg(slot_row + i)) >= R) {
+            const uint32_t s = uint32_t(i) / share;
+            atomicOr(&parts[s >> 5], 1u << (s & 31u));
         }
+    __syncthreads();
+    uint32_t before = 0u, all = 0u;
+    for (uint32_t w = 0; w < kMaxClears / 32; ++w) {
+        all += __popc(parts[w]);
+        if (w < blockIdx.x >> 5) before += __popc(parts[w]);
+        if (w == blockIdx.x >> 5) before += __popc(parts[w] & ((1u << (blockIdx.x & 31u)) - 1u));
+    }
+    const uint32_t part = min(((R + all - 1) / all + 31u) & ~31u, uint32_t(kMarkedRows));
+    for (uint32_t first = before * part; first < R; first += all * part) {
+        const uint32_t rows = min(R - first, part);
+        for (uint32_t w = threadIdx.x; w < part / 32; w += kThreads) named[w] = 0u;
+        __syncthreads();
+#pragma unroll 4
+        for (int32_t i = threadIdx.x; i < n; i += kThreads) {
+            const uint32_t r = named_row(__ldg(slot_row + i)) - first;
+            if (r < rows) atomicOr(&named[r >> 5], 1u << (r & 31u));
+        }
+        __syncthreads();
+        for (uint32_t k = 0; k < rows; k += 32) {
+            uint32_t left = ~named[k >> 5];
+            if (rows - k < 32u) left &= (1u << (rows - k)) - 1u;
+            for (; left; left &= left - 1u) {
+                V* row = out + (int64_t(first + k) + __ffs(int(left)) - 1) * row_len;
+                for (int32_t c = threadIdx.x; c < row_len; c += kThreads) row[c] = V{};
+            }
+        }
+        __syncthreads();
     }
 }
 
@@ -205,15 +219,16 @@ __device__ __forceinline__ Place place(const RowParams& p, uint32_t g, int tpt_l
 }
 
 // ---- dispatch: a copy, V the unit (16 bytes, or one element when rows are not
-// 16-byte aligned), one item per CTA
+// 16-byte aligned), one item per CTA; eight CTAs an SM (with 34 registers instead of
+// 32 there are six: 9.4 us against 9.2)
 template <typename V, int U, int kLog>
-__global__ void __launch_bounds__(kThreads) dispatch_kernel(const RowParams p, int32_t nv, int64_t ldv, int tpt_log_,
+__global__ void __launch_bounds__(kThreads, 8) dispatch_kernel(const RowParams p, int32_t nv, int64_t ldv, int tpt_log_,
                                                             uint32_t chunks, uint32_t clears) {
     const int tpt_log = kLog > 0 ? kLog : tpt_log_;
     griddep_wait();  // x and slot_row may be the previous kernel's output, x_r its input
     if (threadIdx.x == 0) griddep_launch_dependents();
     if (blockIdx.x < clears) {
-        clear_unnamed(p.slot_row, int32_t(p.T * p.top_k), uint32_t(p.R), static_cast<V*>(p.out), nv);
+        clear_unnamed(p.slot_row, int32_t(p.T * p.top_k), uint32_t(p.R), clears, static_cast<V*>(p.out), nv);
         return;
     }
     const int tpt = 1 << tpt_log, lane = threadIdx.x & (tpt - 1);
@@ -317,7 +332,8 @@ __global__ void __launch_bounds__(kThreads) combine_backward_kernel(const RowPar
     if (blockIdx.x < clears) {
         // whole words where the rows are known to be aligned
         using V = std::conditional_t<E == 1, std::conditional_t<sizeof(TY) == 4, uint32_t, uint16_t>, uint4>;
-        clear_unnamed(p.slot_row, int32_t(p.T * p.top_k), uint32_t(p.R), reinterpret_cast<V*>(d_y), int32_t(p.H * sizeof(TY) / sizeof(V)));
+        clear_unnamed(p.slot_row, int32_t(p.T * p.top_k), uint32_t(p.R), clears, reinterpret_cast<V*>(d_y),
+                      int32_t(p.H * sizeof(TY) / sizeof(V)));
         return;
     }
     for (uint32_t g = blockIdx.x - clears; g < items; g += gridDim.x - clears) {

@@ -178,3 +178,52 @@ def test_prompts(cuda_device, T, k, H, dt, out, none, drop):
     assert np.all(np.abs(got - comb) <= _half_step(comb, out, k * 2.0 ** -24 * comb_mag))
     assert np.all(np.abs(back - plain) <= _half_step(plain, dt, k * 2.0 ** -24 * plain_mag))
     assert bgq.device_status() == 0
+
+
+@pytest.mark.parametrize("T,k,H", [(20000, 2, 24), (9000, 4, 17), (70000, 1, 8), (600000, 2, 8)])
+@pytest.mark.parametrize("missing", ["one", "last", "few", "most", "all"])
+def test_unnamed_rows_among_many(cuda_device, T, k, H, missing):
+    """More rows than are marked at a time, more than the CTAs that look for missing slots; one slot without a row, in
+    one share of the slots or in all."""
+    n = T * k
+    rng = np.random.default_rng(T)
+    sr = rng.permutation(n).astype(np.int32)
+    if missing == "one":
+        sr[n // 3] = -1
+    elif missing == "last":
+        sr[-1] = n + 5  # outside: reported, and none
+    else:
+        sr[rng.random(n) < dict(few=0.001, most=0.9, all=2.0)[missing]] = -1
+    named = (sr >= 0) & (sr < n)
+    x = torch.randn(T, H, generator=torch.Generator().manual_seed(T)).to(torch.bfloat16)
+    ref = torch.zeros(n, H, dtype=torch.bfloat16)
+    ref[sr[named].astype(np.int64)] = x[np.nonzero(named)[0] // k]
+    slot_row, xd = torch.from_numpy(sr.reshape(T, k)).to(cuda_device), x.to(cuda_device)
+    bgq.device_status(clear=True)
+    _poison(n * H * 2)
+    x_r = bgq.moe_dispatch(xd, slot_row)
+    assert torch.equal(x_r.cpu(), ref)
+    _poison(n * H * 2)
+    d_y, _ = bgq.moe_combine_backward(xd, x_r, torch.ones(T, k, device=cuda_device), slot_row)
+    assert torch.equal(d_y.cpu(), ref)
+    torch.cuda.synchronize()
+    assert bgq.device_status(clear=True) == (INVALID_ARG if missing == "last" else 0)
+
+
+def test_kept_rows_only(cuda_device):
+    """A result of fewer rows than slots (those of the kept slots): what is not named there is zero too."""
+    T, k, H, R = 3000, 2, 40, 4100
+    rng = np.random.default_rng(2)
+    order = rng.permutation(T * k).astype(np.int32)
+    sr = np.where(order < R, order, -2 - order).reshape(T, k)  # rows behind the kept ones: to be cleared, but outside
+    sr[7, 1] = -1
+    sr[1234, 0] = -1
+    y = torch.randn(R, H, generator=torch.Generator().manual_seed(1)).to(cuda_device)
+    d, w = torch.randn(T, H, device=cuda_device), torch.rand(T, k, device=cuda_device)
+    _poison(R * H * 4)
+    d_y, d_w = bgq.moe_combine_backward(d, y, w, torch.from_numpy(sr).to(cuda_device))
+    ref = torch.zeros(R, H, device=cuda_device)
+    t, s = np.nonzero(sr >= 0)
+    ref[torch.from_numpy(sr[sr >= 0].astype(np.int64)).to(cuda_device)] = w[t, s][:, None] * d[t]
+    assert torch.equal(d_y, ref) and torch.isfinite(d_w).all()
+    assert bgq.device_status() == 0
