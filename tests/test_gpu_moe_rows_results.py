@@ -227,3 +227,14 @@ def test_kept_rows_only(cuda_device):
     ref[torch.from_numpy(sr[sr >= 0].astype(np.int64)).to(cuda_device)] = w[t, s][:, None] * d[t]
     assert torch.equal(d_y, ref) and torch.isfinite(d_w).all()
     assert bgq.device_status() == 0
+
+
+def test_no_rows_at_all(cuda_device):
+    """Every slot dropped and the experts' outputs empty: zeros, and no row to write."""
+    sr = torch.from_numpy(np.array([[-2, -1], [-3, -4]], np.int32)).to(cuda_device)
+    y, w, d = (torch.ones(s, device=cuda_device) for s in ((0, 40), (2, 2), (2, 40)))
+    assert torch.all(bgq.moe_combine(y, w, sr) == 0.0)
+    d_y, d_w = bgq.moe_combine_backward(d, y, w, sr)
+    assert d_y.shape == (0, 40) and torch.all(d_w == 0.0)
+    assert torch.all(bgq.moe_dispatch(d, sr) == 0.0)
+    assert bgq.device_status() == 0
