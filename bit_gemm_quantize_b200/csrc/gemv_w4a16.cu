@@ -62,8 +62,8 @@
 //
 // Measured (in a row, weights from HBM): K = 4096, N = 22016: one token 12.2 us
 // (7.4 us of HBM at the copy rate; the first weights are requested only after the
-// previous kernel has ended), 3 tokens 14.9, 8 tokens 20.9 to 22.3, 16 tokens (two
-// passes) 36; K = 11008, N = 4096, 8 tokens 18.8; two of eight experts of K = 4096,
+// previous kernel has ended), 3 tokens 14.8, 8 tokens 20.8 to 22.6, 16 tokens (two
+// passes) 36; K = 11008, N = 4096, 8 tokens 19.0; two of eight experts of K = 4096,
 // N = 14336 for one token 16.4 (9.4 of HBM), all eight for 16 tokens 50 to 59 as the
 // routing has it (39).  Two CTAs of 8 warps on an SM were slower (13.7 us at one token).
 #include <cooperative_groups.h>
@@ -155,10 +155,9 @@ __device__ __forceinline__ void load_tokens(const void* x, int type, int64_t at,
 // Whether a block of a token (laid out as for block_digits, E the exponent field of
 // its largest magnitude, 2^(E - 127) = P) has values that digits would cut and is held
 // up by so few large ones that the cut may count: with every magnitude taken at most
-// as c = 2^-8 P, its nonzero values average less than c / 4.
-__device__ __forceinline__ bool few_large(float v0, float v1, float v2, float v3, float v4, float v5, float v6, float v7,
-                                       int type, int E) {
-    const float v[8] = {v0, v1, v2, v3, v4, v5, v6, v7};
+// as c = 2^-8 P, its nonzero values average less than c / 4.  `small`: the lanes without
+// a large value; a block without such lanes has no need to be looked at.
+__device__ __forceinline__ bool few_large(const float (&v)[8], int type, int E, unsigned small) {
     // magnitudes from 2^-6 P (fp32), 2^-19 P (fp16) and 2^-22 P (bf16) on keep all their bits
     const uint32_t keep = uint32_t(max(E - (type == kElemF32 ? 6 : type == kElemF16 ? 19 : 22), 1)) << 23;
     const float inv_c = __uint_as_float(uint32_t(262 - E) << 23);
@@ -174,7 +173,7 @@ __device__ __forceinline__ bool few_large(float v0, float v1, float v2, float v3
     for (int o = 1; o < 32; o <<= 1)
         if (o != 4) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     const unsigned lanes = (threadIdx.x & 4) ? 0xF0F0F0F0u : 0x0F0F0F0Fu;  // the block's
-    return (__ballot_sync(0xffffffffu, cut) & lanes) != 0u && sum < 0.0f;
+    return (__ballot_sync(0xffffffffu, cut) & lanes) != 0u && (small & lanes) != 0u && sum < 0.0f;
 }
 
 // A block of 128 values of one token, 8 per lane of 16 lanes (those of the warp
@@ -194,9 +193,10 @@ __device__ __forceinline__ float2 block_digits(const float (&v)[8], int type, ui
     for (int o = 1; o < 32; o <<= 1)
         if (o != 4) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
     const int E = max(int(top >> 23), 19);  // below, the factor would leave the fp32 range
-    // no need to look closer while every lane's eight values have a large one
-    if (!__all_sync(0xffffffffu, own >= uint32_t(E - 10) << 23))
-        plain = few_large(v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7], type, E);
+    // no need to look closer while every lane's eight values have a large one (a block's
+    // answer is its own: the warp's other block must not change it)
+    const unsigned small = __ballot_sync(0xffffffffu, own < uint32_t(E - 10) << 23);
+    if (small) plain = few_large(v, type, E, small);
     uint32_t y[8];
     float2 F;
     if (E < 255) {
@@ -886,7 +886,7 @@ cudaError_t launch_t(Params& p, int num_sms, cudaStream_t stream) {
     // CTAs that split K: so many that making the tokens' digits stays short, 128
     // (token, block) pairs in a CTA (64 where a pass of 8 tokens is bound by its
     // arithmetic).  K = 11008, N = 4096, 8 tokens: 39.8 us with one CTA, 28.7 with 2,
-    // 21.2 with 4, 18.8 with 8; K = 4096, N = 22016: 3 tokens 14.8 with one, 15.7 with 2;
+    // 21.2 with 4, 19.0 with 8; K = 4096, N = 22016: 3 tokens 14.8 with one, 15.7 with 2;
     // 8 tokens 32.2 with one, 22.3 with 2, 20.9 with 4.
     const int nkb = p.K / 128;
     p.max_rows = int(p.R < kRows ? p.R : kRows);

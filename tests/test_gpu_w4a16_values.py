@@ -310,3 +310,23 @@ def test_graph_and_streams_with_tokens_in_fp32(cuda_device):
         for got, ref in ((y, want[i]), (beside, want[1 - i])):
             assert torch.equal(torch.nan_to_num(got, nan=7.0), torch.nan_to_num(ref, nan=7.0))
             assert torch.equal(torch.isnan(got), torch.isnan(ref))
+
+
+@pytest.mark.parametrize("form", ["dense", "experts"])
+@pytest.mark.parametrize("M,K", [(2, 128), (3, 384), (4, 128), (8, 128), (7, 640)])
+def test_a_token_in_fp32_leaves_its_neighbours(cuda_device, form, M, K):
+    """Beside a token that is multiplied in fp32, one at the border (every eight values hold a large one, nearly all others
+    are tiny) gives the same bits as beside ordinary tokens."""
+    rng = np.random.default_rng(M)
+    N = 40
+    x = rng.standard_normal((M, K)) * 2.0 ** -13
+    x[:, ::8] = rng.uniform(1.0, 1.9, (M, K // 8)) * 2.0 ** -9
+    x[:, ::128] = 1.5
+    q, scale = rng.integers(-8, 8, (N, K)), _scales(rng, K, N, "float")
+    for bad in range(M):
+        other = x.copy()
+        other[bad] = rng.standard_normal(K) * 1e-6
+        other[bad, 5::128] = 3e4
+        a, b = (torch.from_numpy(v.astype(np.float32)).to(cuda_device) for v in (x, other))
+        keep = [m for m in range(M) if m != bad]
+        assert torch.equal(_call(form, a, q, scale, "float")[keep], _call(form, b, q, scale, "float")[keep]), bad
