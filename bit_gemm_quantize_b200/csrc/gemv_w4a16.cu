@@ -62,8 +62,8 @@
 //
 // Measured (in a row, weights from HBM): K = 4096, N = 22016: one token 12.2 us
 // (7.4 us of HBM at the copy rate; the first weights are requested only after the
-// previous kernel has ended), 3 tokens 14.8, 8 tokens 20.8 to 22.6, 16 tokens (two
-// passes) 36; K = 11008, N = 4096, 8 tokens 19.0; two of eight experts of K = 4096,
+// previous kernel has ended), 3 tokens 14.9, 8 tokens 20.9 to 21.9, 16 tokens (two
+// passes) 36; K = 11008, N = 4096, 8 tokens 18.6; two of eight experts of K = 4096,
 // N = 14336 for one token 16.4 (9.4 of HBM), all eight for 16 tokens 50 to 59 as the
 // routing has it (39).  Two CTAs of 8 warps on an SM were slower (13.7 us at one token).
 #include <cooperative_groups.h>
@@ -193,10 +193,6 @@ __device__ __forceinline__ float2 block_digits(const float (&v)[8], int type, ui
     for (int o = 1; o < 32; o <<= 1)
         if (o != 4) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
     const int E = max(int(top >> 23), 19);  // below, the factor would leave the fp32 range
-    // no need to look closer while every lane's eight values have a large one (a block's
-    // answer is its own: the warp's other block must not change it)
-    const unsigned small = __ballot_sync(0xffffffffu, own < uint32_t(E - 10) << 23);
-    if (small) plain = few_large(v, type, E, small);
     uint32_t y[8];
     float2 F;
     if (E < 255) {
@@ -227,6 +223,11 @@ __device__ __forceinline__ float2 block_digits(const float (&v)[8], int type, ui
         dig[2][h] = __byte_perm(c, d, 0x5410);
         dig[3][h] = __byte_perm(c, d, 0x7632);
     }
+    // no need to look closer while every lane's eight values have a large one (a block's
+    // answer is its own: the warp's other block must not change it).  Asked here, behind
+    // the digits, it costs less: 8 tokens 18.6 us against 19.0
+    const unsigned small = __ballot_sync(0xffffffffu, own < uint32_t(E - 10) << 23);
+    if (small) plain |= few_large(v, type, E, small);
     return F;
 }
 
@@ -338,7 +339,7 @@ __device__ __forceinline__ void find_plain(const void* x, int type, int64_t ldx,
 // columns, a lane eight codes of each in a chain of products, scaled and added to the
 // lane's sums; the lanes' sums are added last.  The cluster's CTAs share the columns.
 // A token costs about 30 us at K = 4096, N = 22016 (bound by latency); where there is
-// none the kernel is as fast as without this.
+// none, the search for it 0.2 to 0.3 us of 12 to 19.
 template <bool INT>
 __device__ __forceinline__ void plain_tokens(const Params& p, const Run& run, const Rows& rows, uint32_t tokens) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -886,7 +887,7 @@ cudaError_t launch_t(Params& p, int num_sms, cudaStream_t stream) {
     // CTAs that split K: so many that making the tokens' digits stays short, 128
     // (token, block) pairs in a CTA (64 where a pass of 8 tokens is bound by its
     // arithmetic).  K = 11008, N = 4096, 8 tokens: 39.8 us with one CTA, 28.7 with 2,
-    // 21.2 with 4, 19.0 with 8; K = 4096, N = 22016: 3 tokens 14.8 with one, 15.7 with 2;
+    // 21.2 with 4, 18.6 with 8; K = 4096, N = 22016: 3 tokens 14.8 with one, 15.7 with 2;
     // 8 tokens 32.2 with one, 22.3 with 2, 20.9 with 4.
     const int nkb = p.K / 128;
     p.max_rows = int(p.R < kRows ? p.R : kRows);
